@@ -70,6 +70,7 @@ extern "C" {
 #define PKV_ERR_TIMEOUT 0x4  /* a bounded wait (a copy into shared memory, or another CTA's partial) gave up; results incomplete */
 #define PKV_ERR_SPLITS  0x8  /* a row needed more than max_splits partial results: row skipped */
 #define PKV_ERR_POSITION 0x10 /* a RoPE position outside the RoPE table's rows: token skipped, its rows zeroed */
+#define PKV_ERR_NO_PAGES 0x20 /* a step needs more free pages than its list holds: the sequence gets none, its tokens no slot */
 
 typedef struct pkv_pool pkv_pool_t;
 
@@ -399,6 +400,195 @@ int paged_gqa_decode_partials(const pkv_pool_t *pool, const float *q_rot,
  */
 int paged_kv_split_combine(const float *o_part, const float *lse_part, const int32_t *num_splits,
                            float *out, int rows, int max_splits, int head_dim, void *stream);
+
+/* Largest batch paged_tables_build serves. */
+#define PKV_TABLES_MAX_BATCH 8192
+
+/*
+ * A step's block tables, slot maps and positions, built on the GPU from the
+ * requests' lengths and a list of free pages. Sequence b holds start_pos[b]
+ * cached tokens and brings new_tokens[b] (0 or more; 1 for a decode, a chunk
+ * for a prefill). With have = ceil(start/16), need = ceil((start+new)/16) -
+ * have and base_b the sum of need over the sequences before b, block have + i
+ * (i < need) of (layer l, sequence b) becomes
+ *     free_pages[*free_head + base_b * num_layers + l * need + i],
+ * and the step's token t (sequence b, the (t - cu_tokens[b])-th it brings, at
+ * position p = start + t - cu_tokens[b]) gets, in layer l, slot
+ * block_tables[l][b][p / 16] * 16 + p % 16 of the pool.
+ *   start_pos, new_tokens  int32 [batch], batch <= PKV_TABLES_MAX_BATCH
+ *   free_pages   int32 [num_free]: ids of free pages, used from entry
+ *                *free_head on
+ *   free_head    int32 [1], 0 <= *free_head <= num_free;  free_head_out int32
+ *                [1] out: the next unused entry. They must not be the same
+ *                word: pass the one step's output as the next one's input.
+ *   block_tables int32 [num_layers][batch][max_blocks], in and out: the new
+ *                blocks' entries are written, the others kept
+ *   cu_tokens    int32 [batch+1] out: first token of each sequence, the last
+ *                one the step's token count, capacity or not (counts stop at
+ *                2^30 - 1)
+ *   seq_lens     int32 [batch] out: tokens after the step (start + new, or
+ *                start where the sequence is not served)
+ *   positions    int32 [capacity] out;  slot_map int32 [num_layers][capacity]
+ *                out: position 0 and slot -1 for entries past the step's
+ *                tokens and for tokens of a sequence that is not served.
+ *                capacity < 2^29.
+ * A sequence is not served, and takes no pages, when a length is negative,
+ * start + new passes max_blocks*16 or its tokens end past capacity
+ * (PKV_ERR_SEQ_LEN), or when it needs pages and the list does not hold those
+ * of all sequences up to and including it (PKV_ERR_NO_PAGES; sequences are
+ * served in order). A page id outside the pool is stored as -1, its tokens
+ * get slot -1 (PKV_ERR_PAGE_ID). One launch. (Not on the pages: their engine
+ * keeps the tables on the host, as pkv_sched.h does.)
+ */
+int paged_tables_build(pkv_pool_t *pool, const int32_t *start_pos, const int32_t *new_tokens,
+                       int batch, int num_layers, const int32_t *free_pages, int num_free,
+                       const int32_t *free_head, int32_t *free_head_out, int32_t *block_tables,
+                       int max_blocks, int32_t *cu_tokens, int32_t *seq_lens, int32_t *positions,
+                       int32_t *slot_map, int capacity, void *stream);
+
+/*
+ * A RoPE table (layout of paged_rope_cos_sin) of positions 0 ..
+ * num_positions - 1 for given frequencies: entry j < num_freqs of row p holds
+ * magnitude times the cos and sin of fl64(p * inv_freq[j]), the product by
+ * magnitude rounded once more to fp64 (exact for 1); entries from num_freqs on
+ * have angle 0. With inv_freq[j] = theta^(-2j/64), 32 frequencies and
+ * magnitude 1 it is the table of paged_rope_table_build. Scaled rotary
+ * positions (interpolated, by wavelength band, with an attention factor) are
+ * such frequencies and magnitudes.
+ *   inv_freq  HOST pointer, double [num_freqs], finite; 1 <= num_freqs <= 32
+ *   magnitude finite
+ */
+int paged_rope_table_build_freqs(const double *inv_freq, int num_freqs, double magnitude,
+                                 int num_positions, void *table, void *stream);
+
+/*
+ * RoPE of a step's q and k in either pairing, of all or part of the head,
+ * with the append of k and v, for one layer. Pair j < rot_dim/2 of a head is
+ * dims (j, j + rot_dim/2), or (2j, 2j+1) when interleaved != 0; it is rotated
+ * by entry j of the table row of the token's position. Dims from rot_dim on
+ * are passed through.
+ *   q, k, v    bf16 [tokens][heads][64], 8-byte aligned; token t's heads start
+ *              at element t * q_stride (k_stride, v_stride), so that they may
+ *              be slices of one projection's output. Strides are multiples
+ *              of 4 elements, at least heads * 64.
+ *   q_rot      fp32 [tokens][num_q_heads][64] out, 16-byte aligned
+ *   slot_map   int32 [tokens], this layer's slots (paged_tables_build): page *
+ *              16 + slot. A token with a negative slot is rotated, not stored.
+ *   positions  int32 [tokens], rows of rope_table
+ *   rot_dim    8, 16, .. 64
+ * The stored key is rounded to bf16 once, exactly as paged_kv_append_rope
+ * rounds it (with rot_dim 64, half pairs and an unscaled table the bytes are
+ * the same); v is copied bit for bit. A position outside the table's rows
+ * skips the token (its q_rot rows zeroed, nothing stored, PKV_ERR_POSITION);
+ * a slot past the pool is not stored to (PKV_ERR_PAGE_ID).
+ */
+int paged_rope_append(pkv_pool_t *pool, const void *q, long long q_stride, const void *k,
+                      long long k_stride, const void *v, long long v_stride, float *q_rot,
+                      const int32_t *slot_map, const int32_t *positions, int tokens,
+                      int num_q_heads, const void *rope_table, int rope_positions, int rot_dim,
+                      int interleaved, void *stream);
+
+/*
+ * How attention scores are made and which keys a query sees. With query
+ * position i and key position j of one sequence, the score is
+ *     s = scale * q.k;  s = softcap * tanh(s / softcap) if softcap > 0;
+ *     s = s - alibi_slopes[head] * |i - j| if alibi_slopes,
+ * and key j is seen when it is in the sequence and j <= i (or j is in the
+ * sequence's prefix), j > i - window if window > 0, and j is not before the
+ * first key the query may see. A query that sees no key gets a zero row.
+ */
+typedef struct pkv_scoring {
+  float scale;               /* softmax scale, finite */
+  float softcap;             /* 0: scores are not capped; otherwise > 0, finite */
+  const float *alibi_slopes; /* fp32 [num_q_heads] on the device, or NULL */
+  int window;                /* 0: no window; otherwise the last `window` positions, itself included */
+} pkv_scoring_t;
+
+/* Types of an attention output or of logits. */
+#define PKV_BF16 0
+#define PKV_F32 1
+
+/*
+ * paged_gqa_decode with pkv_scoring scores: attention of one token a sequence,
+ * at position seq_lens[b] - 1, over its cached pages. Pages before the first
+ * key that a sequence sees are neither read nor looked up (they may have been
+ * given back).
+ *   first_keys   int32 [batch] or NULL: first key position each sequence sees
+ *                (the start of its document, or of what is kept)
+ *   out          [batch][num_q_heads][64] of out_type (PKV_BF16: the fp32
+ *                result rounded once), 16-byte aligned
+ *   other arguments as for paged_gqa_decode (the automatic partition; the
+ *   workspace is sized with pages_per_split = 0). max_blocks <= 2^23.
+ */
+int paged_gqa_decode_scored(const pkv_pool_t *pool, const float *q_rot, void *out, int out_type,
+                            const int32_t *block_tables, int max_blocks, const int32_t *seq_lens,
+                            const int32_t *first_keys, int batch, int num_q_heads,
+                            const pkv_scoring_t *scoring, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/*
+ * The attention of paged_prefill with pkv_scoring scores, over pages that
+ * already hold the chunk's keys and values (paged_rope_append). Token t of
+ * sequence b's chunk is at position start_pos[b] + t; the sequence ends with
+ * its chunk.
+ *   q_rot        fp32 [total_tokens][num_q_heads][64], 16-byte aligned
+ *   out          [total_tokens][num_q_heads][64] of out_type, 16-byte aligned
+ *   prefix_lens  int32 [batch] or NULL: keys below prefix_lens[b] are seen by
+ *                queries before them too (a prefix that attends both ways)
+ *   doc_starts   int32 [total_tokens] or NULL: first key position each chunk
+ *                token sees (the start of its document)
+ *   block_tables, cu_tokens, start_pos, workspace: as for paged_prefill
+ *   (the workspace is sized by paged_prefill_workspace_bytes).
+ * Rows of tokens past the block table's end, or of a sequence with a negative
+ * start, are zeroed (PKV_ERR_SEQ_LEN); rows of no chunk are not written; a bad
+ * page's keys are skipped (PKV_ERR_PAGE_ID).
+ * Pages before the first key that a tile of rows sees (of at most 128 / group
+ * tokens) are neither read nor looked up.
+ * A value that is not finite can reach the rows of neighbouring tokens of its
+ * sequence (of one tile) that do not see it; slots outside every row's keys
+ * may hold anything. Two launches.
+ */
+int paged_gqa_prefill_scored(const pkv_pool_t *pool, const float *q_rot, void *out, int out_type,
+                             const int32_t *block_tables, int max_blocks, const int32_t *cu_tokens,
+                             const int32_t *start_pos, const int32_t *prefix_lens,
+                             const int32_t *doc_starts, int batch, int total_tokens,
+                             int num_q_heads, const pkv_scoring_t *scoring, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* Largest number of alternatives token_logprobs gives. */
+#define PKV_MAX_TOP 32
+
+/* Device bytes of workspace token_logprobs needs (0 for invalid sizes). */
+size_t token_logprobs_workspace_bytes(int rows, int vocab, int top);
+
+/*
+ * Log-probabilities of given tokens, with the entropy of each row's
+ * distribution and its most likely tokens. With y = scale * logits[r] and
+ * lse = log sum_v exp(y_v):
+ *   logprobs[r]        = y_{targets[r]} - lse (NaN for a target outside
+ *                        [0, vocab))
+ *   entropy[r]         = -sum_v p_v log p_v, p_v = exp(y_v - lse), in nats
+ *   top_ids[r][i]      the i-th largest logit's token, the lower id first
+ *                        among equals;  top_logprobs[r][i] its log-probability
+ *   logits   bf16 or fp32 (logits_type) [rows][vocab], row r at element
+ *            r * row_stride; any alignment of the element
+ *   scale    1 / temperature, 1e-6 .. 1e6
+ *   targets  int32 [rows] with logprobs fp32 [rows], or both NULL
+ *   entropy  fp32 [rows] or NULL
+ *   top      0 .. min(PKV_MAX_TOP, vocab); top_ids int32 [rows][top] and
+ *            top_logprobs fp32 [rows][top] (NULL when top is 0)
+ *   workspace  device memory of at least token_logprobs_workspace_bytes(),
+ *            256-byte aligned, ZERO-FILLED before its first use (each call
+ *            leaves what it needs to be zero at zero). Calls that share a
+ *            workspace must not overlap on the GPU.
+ * A logit of -inf is a token of probability 0. A row that holds +inf or NaN,
+ * or only -inf, has no distribution: its logprobs, entropy and top_logprobs
+ * are NaN; top_ids still follow the order of its logits, NaN taken as -inf.
+ */
+int token_logprobs(const void *logits, int logits_type, long long row_stride, int rows, int vocab,
+                   float scale, const int32_t *targets, int top, float *logprobs, float *entropy,
+                   int32_t *top_ids, float *top_logprobs, void *workspace, size_t workspace_bytes,
+                   void *stream);
 
 /*
  * Read the pool's device error word (PKV_ERR_* bits) into *bits; with reset

@@ -9,6 +9,7 @@ with page-budget admission (``pkv_sched_*``, include/pkv_sched.h). This package
 is the thin Python binding with the same names; it only marshals arguments.
 """
 from ._binding import (  # noqa: F401
+    ERR_NO_PAGES,
     ERR_PAGE_ID,
     ERR_POSITION,
     ERR_SEQ_LEN,
@@ -18,10 +19,13 @@ from ._binding import (  # noqa: F401
     HEAD_DIM,
     LIBRARY,
     MAX_GROUP,
+    MAX_TOP,
     PAGE_SIZE,
+    TABLES_MAX_BATCH,
     KVPool,
     PkvError,
     alloc_decode_workspace,
+    alloc_logprobs_workspace,
     alloc_prefill_workspace,
     alloc_rope_table,
     build_rope_table,
@@ -37,17 +41,25 @@ from ._binding import (  # noqa: F401
     paged_gqa_decode,
     paged_gqa_decode_no_alloc,
     paged_gqa_decode_partials,
+    paged_gqa_decode_scored,
     paged_gqa_decode_workspace_bytes,
+    paged_gqa_prefill_scored,
     paged_kv_append_rope,
     paged_kv_split_combine,
     paged_prefill,
     paged_prefill_workspace_bytes,
+    paged_rope_append,
     paged_rope_cos_sin,
     paged_rope_table_build,
+    paged_rope_table_build_freqs,
+    paged_tables_build,
     rope_table_rows,
     pkv_get_error,
     pkv_last_cuda_error,
+    token_logprobs,
+    token_logprobs_workspace_bytes,
 )
+from .rope import rope_frequencies  # noqa: F401
 from .sched import (  # noqa: F401
     PageScheduler,
     pkv_sched_admit,

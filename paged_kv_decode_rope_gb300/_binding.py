@@ -20,10 +20,14 @@ PAGE_SIZE = 16
 MAX_GROUP = 8
 ROPE_TABLE_BYTES_PER_ROW = 1024  # PKV_ROPE_TABLE_BYTES(1)
 ERR_SEQ_LEN, ERR_PAGE_ID, ERR_TIMEOUT, ERR_SPLITS, ERR_POSITION = 0x1, 0x2, 0x4, 0x8, 0x10
+ERR_NO_PAGES = 0x20
+TABLES_MAX_BATCH = 8192
+MAX_TOP = 32
 
 _lib = None
 _lock = threading.Lock()
 
+_ll = ctypes.c_longlong
 _vp, _i, _sz, _f, _d = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_double
 
 _SIGNATURES = {
@@ -46,6 +50,14 @@ _SIGNATURES = {
     "paged_prefill_workspace_bytes": (_sz, [_i, _i, _i]),
     "paged_prefill": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _vp, _i, _f,
                            _vp, _sz, _vp]),
+    "paged_tables_build": (_i, [_vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _vp]),
+    "paged_rope_table_build_freqs": (_i, [_vp, _i, _d, _i, _vp, _vp]),
+    "paged_rope_append": (_i, [_vp, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _i, _i, _vp, _i, _i, _i, _vp]),
+    "paged_gqa_decode_scored": (_i, [_vp, _vp, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp]),
+    "paged_gqa_prefill_scored": (_i, [_vp, _vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _sz,
+                                      _vp]),
+    "token_logprobs_workspace_bytes": (_sz, [_i, _i, _i]),
+    "token_logprobs": (_i, [_vp, _i, _ll, _i, _i, _f, _vp, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "pkv_get_error": (_i, [_vp, ctypes.POINTER(_i), _i]),
     "pkv_last_cuda_error": (_i, []),
     # include/pkv_sched.h (host only)
@@ -60,6 +72,14 @@ _SIGNATURES = {
     "pkv_sched_note_batch": (_i, [_vp, _i]),
     "pkv_sched_stats": (_i, [_vp, _vp]),
 }
+
+
+class _Scoring(ctypes.Structure):
+    """pkv_scoring_t."""
+    _fields_ = [("scale", _f), ("softcap", _f), ("alibi_slopes", _vp), ("window", _i)]
+
+
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}  # PKV_BF16, PKV_F32
 
 
 class PkvError(RuntimeError):
@@ -435,6 +455,204 @@ def paged_kv_split_combine(o_part: torch.Tensor, lse_part: torch.Tensor, num_spl
         _dev(num_splits, torch.int32, "num_splits", 1), _dev(out, torch.float32, "out"),
         rows, max_splits, head_dim, _stream(stream))
     _check("paged_kv_split_combine", rc)
+
+
+def _arg(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str) -> int:
+    """The pointer of a contiguous CUDA tensor of exactly this type and shape
+    (the checks of _shape and _dev, at the price of one when they hold)."""
+    if type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _shape(t, shape, name)
+    return _dev(t, dtype, name)
+
+
+def _optional(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, name: str) -> int | None:
+    return None if t is None else _arg(t, dtype, shape, name)
+
+
+def _raw_stream(stream, t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else _stream(stream)
+
+
+def _typed(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    try:
+        return _TYPES[t.dtype]
+    except KeyError:
+        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}") from None
+
+
+def paged_tables_build(pool: KVPool, start_pos: torch.Tensor, new_tokens: torch.Tensor,
+                       free_pages: torch.Tensor, free_head: torch.Tensor, free_head_out: torch.Tensor,
+                       block_tables: torch.Tensor, cu_tokens: torch.Tensor, seq_lens: torch.Tensor,
+                       positions: torch.Tensor, slot_map: torch.Tensor, stream=None) -> None:
+    """A step's block tables, slot maps and positions from its lengths.
+    start_pos/new_tokens [B], free_pages [F], free_head [1] int32;
+    block_tables [L,B,max_blocks] int32 in and out; free_head_out [1] (not
+    free_head itself), cu_tokens [B+1], seq_lens [B], positions [T],
+    slot_map [L,T] int32 out, T the capacity in tokens."""
+    i32 = torch.int32
+    layers, batch, max_blocks = _shape(block_tables, (None, None, None), "block_tables")
+    (capacity,) = _shape(positions, (None,), "positions")
+    (num_free,) = _shape(free_pages, (None,), "free_pages")
+    rc = lib().paged_tables_build(
+        pool.handle, _arg(start_pos, i32, (batch,), "start_pos"), _arg(new_tokens, i32, (batch,), "new_tokens"),
+        batch, layers, _arg(free_pages, i32, (num_free,), "free_pages"), num_free,
+        _arg(free_head, i32, (1,), "free_head"), _arg(free_head_out, i32, (1,), "free_head_out"),
+        _arg(block_tables, i32, (layers, batch, max_blocks), "block_tables"), max_blocks,
+        _arg(cu_tokens, i32, (batch + 1,), "cu_tokens"), _arg(seq_lens, i32, (batch,), "seq_lens"),
+        _arg(positions, i32, (capacity,), "positions"), _arg(slot_map, i32, (layers, capacity), "slot_map"),
+        capacity, _raw_stream(stream, block_tables))
+    if rc:
+        raise PkvError("paged_tables_build", rc)
+
+
+def paged_rope_table_build_freqs(inv_freq, num_positions: int, table: torch.Tensor, magnitude: float = 1.0,
+                                 stream=None) -> None:
+    """The RoPE table of positions 0 .. num_positions-1 for given inverse
+    frequencies (up to 32 numbers, see rope_frequencies), cos and sin
+    multiplied by magnitude."""
+    inv_freq = [float(f) for f in inv_freq]
+    if table.numel() < num_positions * ROPE_TABLE_BYTES_PER_ROW:
+        raise ValueError("rope table too small")
+    rc = lib().paged_rope_table_build_freqs((_d * len(inv_freq))(*inv_freq), len(inv_freq), float(magnitude),
+                                            int(num_positions), _dev(table, torch.uint8, "table", 1),
+                                            _stream(stream))
+    _check("paged_rope_table_build_freqs", rc)
+
+
+def _token_rows(t: torch.Tensor, tokens: int, heads: int, name: str) -> tuple[int, int]:
+    """Pointer and token stride (elements) of bf16 [tokens][heads][64] whose
+    heads are contiguous: the whole tensor, or a slice of a projection."""
+    if type(t) is not torch.Tensor or t.shape != (tokens, heads, HEAD_DIM):
+        _shape(t, (tokens, heads, HEAD_DIM), name)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    stride, head, dim = t.stride()
+    if (dim != 1 or (head != HEAD_DIM and heads > 1)) and tokens > 0:
+        raise ValueError(f"{name} must have contiguous heads")
+    return t.data_ptr(), stride if tokens > 1 else heads * HEAD_DIM
+
+
+def paged_rope_append(pool: KVPool, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_rot: torch.Tensor,
+                      slot_map: torch.Tensor, positions: torch.Tensor, rope_table: torch.Tensor,
+                      rot_dim: int = HEAD_DIM, interleaved: bool = False, stream=None) -> None:
+    """RoPE (the first rot_dim dims, half or interleaved pairs) of q
+    [T,Hq,64] and k [T,Hkv,64] bf16, and the append of k and v at slot_map
+    [T] int32 (one layer's slots; negative: not stored). q_rot [T,Hq,64] fp32
+    out; positions [T] int32, rows of rope_table. q, k and v may be slices of
+    one projection's output (any token stride)."""
+    tokens, hq, _ = _shape(q, (None, None, HEAD_DIM), "q")
+    hkv = pool.num_kv_heads
+    qp, qs = _token_rows(q, tokens, hq, "q")
+    kp, ks = _token_rows(k, tokens, hkv, "k")
+    vp, vs = _token_rows(v, tokens, hkv, "v")
+    rc = lib().paged_rope_append(
+        pool.handle, qp, qs, kp, ks, vp, vs, _arg(q_rot, torch.float32, (tokens, hq, HEAD_DIM), "q_rot"),
+        _arg(slot_map, torch.int32, (tokens,), "slot_map"), _arg(positions, torch.int32, (tokens,), "positions"),
+        tokens, hq, _dev(rope_table, torch.uint8, "rope_table", 1), rope_table_rows(rope_table), int(rot_dim),
+        1 if interleaved else 0, _raw_stream(stream, q))
+    if rc:
+        raise PkvError("paged_rope_append", rc)
+
+
+def _scoring(scale, softcap, alibi_slopes, window, hq):
+    return ctypes.byref(_Scoring(scale, softcap, _optional(alibi_slopes, torch.float32, (hq,), "alibi_slopes"),
+                                 window))
+
+
+def paged_gqa_decode_scored(pool: KVPool, q_rot: torch.Tensor, out: torch.Tensor, block_tables: torch.Tensor,
+                            seq_lens: torch.Tensor, scale: float, workspace: torch.Tensor, softcap: float = 0.0,
+                            alibi_slopes: torch.Tensor | None = None, window: int = 0,
+                            first_keys: torch.Tensor | None = None, stream=None) -> None:
+    """paged_gqa_decode with capped (softcap > 0), distance-biased
+    (alibi_slopes [Hq] fp32) and windowed (window > 0) scores, over keys from
+    first_keys [B] int32 on. q_rot [B,Hq,64] fp32, out [B,Hq,64] fp32 or
+    bf16; workspace from alloc_decode_workspace()."""
+    batch, hq, _ = _shape(q_rot, (None, None, HEAD_DIM), "q_rot")
+    _, max_blocks = _shape(block_tables, (batch, None), "block_tables")
+    out_type = _typed(out, "out")
+    rc = lib().paged_gqa_decode_scored(
+        pool.handle, _arg(q_rot, torch.float32, (batch, hq, HEAD_DIM), "q_rot"),
+        _arg(out, out.dtype, (batch, hq, HEAD_DIM), "out"), out_type,
+        _arg(block_tables, torch.int32, (batch, max_blocks), "block_tables"), max_blocks,
+        _arg(seq_lens, torch.int32, (batch,), "seq_lens"), _optional(first_keys, torch.int32, (batch,), "first_keys"),
+        batch, hq, _scoring(scale, softcap, alibi_slopes, window, hq), _dev(workspace, torch.uint8, "workspace", 1),
+        workspace.numel(), _raw_stream(stream, q_rot))
+    if rc:
+        raise PkvError("paged_gqa_decode_scored", rc)
+
+
+def paged_gqa_prefill_scored(pool: KVPool, q_rot: torch.Tensor, out: torch.Tensor, block_tables: torch.Tensor,
+                             cu_tokens: torch.Tensor, start_pos: torch.Tensor, scale: float,
+                             workspace: torch.Tensor, softcap: float = 0.0,
+                             alibi_slopes: torch.Tensor | None = None, window: int = 0,
+                             prefix_lens: torch.Tensor | None = None, doc_starts: torch.Tensor | None = None,
+                             stream=None) -> None:
+    """The attention of chunks whose keys are already in the pool, with
+    capped, distance-biased and windowed scores (as paged_gqa_decode_scored),
+    prefixes that attend both ways (prefix_lens [B] int32) and packed
+    documents (doc_starts [T] int32, each token's first visible position).
+    q_rot [T,Hq,64] fp32, out [T,Hq,64] fp32 or bf16, block_tables
+    [B,max_blocks], cu_tokens [B+1], start_pos [B] int32; workspace from
+    alloc_prefill_workspace()."""
+    total, hq, _ = _shape(q_rot, (None, None, HEAD_DIM), "q_rot")
+    batch, max_blocks = _shape(block_tables, (None, None), "block_tables")
+    i32 = torch.int32
+    out_type = _typed(out, "out")
+    rc = lib().paged_gqa_prefill_scored(
+        pool.handle, _arg(q_rot, torch.float32, (total, hq, HEAD_DIM), "q_rot"),
+        _arg(out, out.dtype, (total, hq, HEAD_DIM), "out"), out_type,
+        _arg(block_tables, i32, (batch, max_blocks), "block_tables"), max_blocks,
+        _arg(cu_tokens, i32, (batch + 1,), "cu_tokens"), _arg(start_pos, i32, (batch,), "start_pos"),
+        _optional(prefix_lens, i32, (batch,), "prefix_lens"), _optional(doc_starts, i32, (total,), "doc_starts"),
+        batch, total, hq, _scoring(scale, softcap, alibi_slopes, window, hq),
+        _dev(workspace, torch.uint8, "workspace", 1), workspace.numel(), _raw_stream(stream, q_rot))
+    if rc:
+        raise PkvError("paged_gqa_prefill_scored", rc)
+
+
+def token_logprobs_workspace_bytes(rows: int, vocab: int, top: int) -> int:
+    return lib().token_logprobs_workspace_bytes(rows, vocab, top)
+
+
+def alloc_logprobs_workspace(rows: int, vocab: int, top: int, device=None) -> torch.Tensor:
+    """A zero-filled workspace for token_logprobs on up to `rows` rows (each
+    call leaves it ready for the next)."""
+    n = token_logprobs_workspace_bytes(rows, vocab, top)
+    if n == 0:
+        raise ValueError("invalid logprobs sizes")
+    return torch.zeros(n, dtype=torch.uint8, device=device or torch.device("cuda"))
+
+
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None, logprobs: torch.Tensor | None,
+                   entropy: torch.Tensor | None, top_ids: torch.Tensor | None,
+                   top_logprobs: torch.Tensor | None, workspace: torch.Tensor, scale: float = 1.0,
+                   stream=None) -> None:
+    """Log-probabilities of targets [R] int32 under logits [R,V] (bf16 or
+    fp32, rows at any stride) times scale, into logprobs [R] fp32; the
+    entropy [R] fp32 of each row; its K most likely tokens top_ids [R,K] int32
+    with top_logprobs [R,K] fp32 (K up to 32, the lower id first among
+    equals). Outputs that are None are left out."""
+    rows, vocab = _shape(logits, (None, None), "logits")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    stride, step = logits.stride()
+    if step != 1 and vocab > 1:
+        raise ValueError("logits must have contiguous rows")
+    top = 0 if top_ids is None else _shape(top_ids, (rows, None), "top_ids")[1]
+    f32, i32 = torch.float32, torch.int32
+    rc = lib().token_logprobs(
+        logits.data_ptr(), _typed(logits, "logits"), stride if rows > 1 else vocab, rows, vocab, scale,
+        _optional(targets, i32, (rows,), "targets"), top, _optional(logprobs, f32, (rows,), "logprobs"),
+        _optional(entropy, f32, (rows,), "entropy"), _optional(top_ids, i32, (rows, top), "top_ids"),
+        _optional(top_logprobs, f32, (rows, top), "top_logprobs"), _dev(workspace, torch.uint8, "workspace", 1),
+        workspace.numel(), _raw_stream(stream, logits))
+    if rc:
+        raise PkvError("token_logprobs", rc)
 
 
 def pkv_get_error(pool: KVPool, reset: bool = False) -> int:

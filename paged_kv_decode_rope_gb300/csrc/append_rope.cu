@@ -129,19 +129,20 @@ __global__ void __launch_bounds__(kAppendThreads) append_rope_kernel(const Appen
 // lo = the remainder rounded to fp32, so hi + lo is within 2^-48 of it) for
 // the fp32 paths of the fused step and the prefill, and in fp64 for their
 // rare fp64 fallback. Small blocks spread the values over as many SMs as the
-// rows allow: each value is a long chain of dependent fp64 operations.
+// rows allow: each value is a long chain of dependent fp64 operations. The
+// values are multiplied by `magnitude` (exact for 1).
 constexpr int kTableThreads = 64;
 __global__ void __launch_bounds__(kTableThreads)
     rope_cos_sin_kernel(const int32_t* __restrict__ positions, int batch, const InvFreq inv,
-                        const RopeSeriesCoef coef, float2* __restrict__ pairs,
-                        double* __restrict__ full) {
+                        const RopeSeriesCoef coef, double magnitude,
+                        float2* __restrict__ pairs, double* __restrict__ full) {
   const int idx = blockIdx.x * blockDim.x + threadIdx.x;  // 2 (b 32 + j) + (0: cos, 1: sin)
   if (idx >= batch * 2 * kHalf) return;
   const int bj = idx >> 1, b = bj / kHalf, j = bj - b * kHalf;
   const int pos = positions ? positions[b] : b;
   bool certain;
-  const double val = rope_cos_or_sin_cr(__dmul_rn(static_cast<double>(pos), inv.v[j]),
-                                        (idx & 1) != 0, coef, &certain);
+  const double val = __dmul_rn(magnitude, rope_cos_or_sin_cr(__dmul_rn(static_cast<double>(pos), inv.v[j]),
+                                                             (idx & 1) != 0, coef, &certain));
   const float hi = __double2float_rn(val);
   pairs[idx] = make_float2(hi, __double2float_rn(__dsub_rn(val, static_cast<double>(hi))));
   full[idx] = val;
@@ -163,19 +164,26 @@ RopeSeriesCoef rope_series_coef() {
   return c;
 }
 
-cudaError_t launch_rope_cos_sin(const int32_t* positions, int batch, double rope_theta,
-                                void* table, cudaStream_t stream) {
-  if (batch == 0) return cudaSuccess;
-  if (static_cast<long long>(batch) * 2 * kHalf >= (1ll << 31)) return cudaErrorInvalidValue;
+cudaError_t launch_rope_table(const int32_t* positions, int rows, const double* inv_freq, double magnitude,
+                              void* table, cudaStream_t stream) {
+  if (rows == 0) return cudaSuccess;
+  if (static_cast<long long>(rows) * 2 * kHalf >= (1ll << 31)) return cudaErrorInvalidValue;
   InvFreq inv;
-  for (int j = 0; j < kHalf; ++j)
-    inv.v[j] = std::pow(rope_theta, -(2.0 * j) / static_cast<double>(kHeadDim));
-  const int n = batch * 2 * kHalf;
+  for (int j = 0; j < kHalf; ++j) inv.v[j] = inv_freq[j];
+  const int n = rows * 2 * kHalf;
   float2* pairs = static_cast<float2*>(table);
   double* full = reinterpret_cast<double*>(pairs + n);
   rope_cos_sin_kernel<<<(n + kTableThreads - 1) / kTableThreads, kTableThreads, 0, stream>>>(
-      positions, batch, inv, rope_series_coef(), pairs, full);
+      positions, rows, inv, rope_series_coef(), magnitude, pairs, full);
   return cudaGetLastError();
+}
+
+cudaError_t launch_rope_cos_sin(const int32_t* positions, int batch, double rope_theta,
+                                void* table, cudaStream_t stream) {
+  double inv[kHalf];
+  for (int j = 0; j < kHalf; ++j)
+    inv[j] = std::pow(rope_theta, -(2.0 * j) / static_cast<double>(kHeadDim));
+  return launch_rope_table(positions, batch, inv, 1.0, table, stream);
 }
 
 cudaError_t launch_append_rope(const AppendLaunch& a, cudaStream_t stream) {

@@ -70,6 +70,7 @@ constexpr int kSpareSms = 4;              // SMs left without a decode CTA (see 
 constexpr int kPageUnits = 4;
 constexpr int kSegUnits = 5;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHalfDim = kHeadDim / 2;
 
 // Kernel modes: decode with split pieces merged by the merge kernel; decode
@@ -78,6 +79,12 @@ constexpr int kHalfDim = kHeadDim / 2;
 constexpr int kModeDecode = 0;
 constexpr int kModePartials = 1;
 constexpr int kModeStep = 2;
+// The decode with scores made by pkv_scoring (capped, biased by distance,
+// limited to a window or to keys from a given one on) and an fp32 or bf16
+// output. A sequence's work starts at the page of its first visible key: its
+// length here counts from that page's first slot, so the pages before it are
+// not part of the work list at all.
+constexpr int kModeScored = 3;
 
 // How much of a stage's copies one issue() call starts (see the kernel).
 constexpr int kIssueAll = 0;
@@ -141,7 +148,30 @@ struct DecodeParams {
   int rope_positions;
   float* q_rot_out;         // fp32 [batch][hq][64] or null
   uint8_t* pool_w;          // the pool's bytes, for the new token's rows
+  // scored mode
+  const int32_t* first_keys;  // [batch] or null
+  const float* slopes;        // [hq] or null
+  int window;                 // 0: none
+  float cap;                  // softcap * log2(e), 0: none (qscale then holds 2 log2(e) scale / softcap)
+  int out_bf16;
 };
+
+// Largest batch of one scored launch: its shared memory holds a third integer
+// a sequence (the first page and first slot it sees) where the others hold two.
+constexpr int kScoredBatchChunk = 1024;
+static_assert(3 * kScoredBatchChunk + 1 <= 2 * kDecodeBatchChunk + 1, "the same shared memory serves both");
+// s_bad bit of a sequence that sees no key (its rows are zeroed, no error)
+constexpr int kEmptySequence = 0x100;
+
+// Two neighbouring outputs (dims 2 i, 2 i + 1 of a row) in the launch's type.
+template <int kMode>
+__device__ __forceinline__ void store_pair(const DecodeParams& p, size_t row, int i, float a, float b) {
+  if (kMode == kModeScored && p.out_bf16) {
+    reinterpret_cast<uint32_t*>(p.out)[row * (kHeadDim / 2) + i] = pack_bf16x2(a, b);
+  } else {
+    reinterpret_cast<float2*>(p.out)[row * (kHeadDim / 2) + i] = make_float2(a, b);
+  }
+}
 
 size_t ring_offset_bytes() {
   // sequence lengths and page prefix sums
@@ -478,13 +508,13 @@ __device__ __forceinline__ bool gather_groups_staged(Piece& all, const Piece& ow
   return __all_sync(kFull, complete);
 }
 
-template <int G>
-__device__ __forceinline__ void store_output(float* out_row0, const Piece& pc, int g8, int tig) {
+template <int G, int kMode>
+__device__ __forceinline__ void store_output(const DecodeParams& p, size_t row0, const Piece& pc, int g8,
+                                             int tig) {
   if (g8 >= G) return;
   const float inv = pc.l > 0.f ? 1.f / pc.l : 0.f;
-  float2* dst = reinterpret_cast<float2*>(out_row0 + g8 * kHeadDim);
 #pragma unroll
-  for (int d = 0; d < 8; ++d) dst[4 * d + tig] = make_float2(pc.acc[d].x * inv, pc.acc[d].y * inv);
+  for (int d = 0; d < 8; ++d) store_pair<kMode>(p, row0 + g8, 4 * d + tig, pc.acc[d].x * inv, pc.acc[d].y * inv);
 }
 
 // Step mode, first page of a piece: rotate the group's raw q rows at the
@@ -598,6 +628,7 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
   using C = Cfg<G>;
   constexpr bool kPartials = kMode == kModePartials;
   constexpr bool kStep = kMode == kModeStep;
+  constexpr bool kScored = kMode == kModeScored;
   constexpr int kW = C::kWarps;
   constexpr int kT = C::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -608,6 +639,7 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
   int* s_warp = reinterpret_cast<int*>(smem + kScanOffset);
   int* s_len = reinterpret_cast<int*>(smem + kHdrBytes);
   int* s_pre = s_len + p.batch;
+  int* s_seen = s_pre + p.batch + 1;  // scored: 16 * first visible page + the first visible slot of it
   __shared__ int s_bad;  // PKV_ERR_SEQ_LEN / PKV_ERR_POSITION of sequences skipped here
   __shared__ int s_plan[kPlanHdr];
   const uint32_t bar0 = smem_addr(smem) + warp * C::kStages * 8;
@@ -645,8 +677,16 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
   }
   for (int b = tid; b < p.batch; b += kT) {
     int bad;
-    const int n = checked_length(p.seq_lens[b], cap, kStep ? p.positions : nullptr, b,
-                                 p.rope_positions, &bad);
+    int n = checked_length(p.seq_lens[b], cap, kStep ? p.positions : nullptr, b,
+                           p.rope_positions, &bad);
+    if constexpr (kScored) {
+      int lo = p.window > 0 ? max(n - p.window, 0) : 0;
+      if (p.first_keys) lo = max(lo, p.first_keys[b]);
+      if (lo >= n) bad |= kEmptySequence;
+      s_seen[b] = lo;
+      n = max(n - lo / kPage * kPage, 0);
+      if (bad) n = 0;
+    }
     if (bad) atomicOr(&s_bad, bad);
     s_len[b] = n;
     if (plan) {
@@ -676,7 +716,9 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
   //        a piece (6) | bad page (7) | last page of the sequence (8) |
   //        page index within the sequence (9+)
   //   bh   sequence * hkv + kv head
-  //   pos  step mode: the sequence's RoPE position (its row of the table)
+  //   pos  step mode: the sequence's RoPE position (its row of the table);
+  //        scored mode: 16 * the distance of the page's first slot from the
+  //        query + the first visible slot of the page
   // The producer (copy issue) runs at most kStages items ahead of the consumer,
   // hence at most one batch ahead; the consumer keeps its own copy.
   int pd_base = 0, pd_y = -1, pd_meta = 0, pd_bh = 0, pd_pos = 0;
@@ -691,7 +733,10 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
     bool bad = false;
     if (item < i1) {
       const Cursor ci = locate(item, s_pre, s_len, p.batch, p.hkv);
-      const int page = __ldg(p.block_tables + static_cast<size_t>(ci.b) * p.max_blocks + ci.pg);
+      const int first_page = kScored ? s_seen[ci.b] / kPage : 0;
+      const int page = __ldg(p.block_tables + static_cast<size_t>(ci.b) * p.max_blocks + first_page + ci.pg);
+      if constexpr (kScored)
+        pd_pos = (ci.len - 1 - ci.pg * kPage) * kPage + (ci.pg == 0 ? s_seen[ci.b] % kPage : 0);
       if (kStep) pd_pos = __ldg(p.positions + ci.b);  // checked with the lengths
       const int nv = min(kPage, ci.len - ci.pg * kPage);
       const int first = (item == i0 || ci.pg == 0) ? 1 : 0;
@@ -765,6 +810,7 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
   uint32_t aq[4][4];  // Q as the A operand, one k-step (16 dims) each: bf16 rows g8, remainders g8+8
   float o[8][4];      // O accumulator, dims 8d..8d+7: rows g8 (from P) and g8+8 (from P's remainder)
   float m_run = -INFINITY, l_run = 0.f;
+  float slope = 0.f;  // scored mode: head g8's ALiBi slope, base 2
 
   // lane 0 finds where range r starts, lane 1 where it ends (this warp's
   // first range: read from the plan when there is one)
@@ -787,12 +833,14 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
   }
 
   if (s_bad) {  // rows of invalid sequences: zero output (or zero split count)
-    if (blockIdx.x == 0 && tid == 0) atomicOr(p.err, s_bad);
+    if (blockIdx.x == 0 && tid == 0 && (s_bad & ~kEmptySequence)) atomicOr(p.err, s_bad & ~kEmptySequence);
     const int rows = p.batch * p.hq;
     for (int idx = blockIdx.x * kT + tid; idx < rows; idx += gridDim.x * kT) {
       if (s_len[idx / p.hq] != 0) continue;
       if (kPartials) {
         p.num_splits[idx] = 0;
+      } else if (kScored) {
+        for (int i = 0; i < kHeadDim / 2; ++i) store_pair<kMode>(p, idx, i, 0.f, 0.f);
       } else {
         if (kStep && p.q_rot_out) {
           float4* qo = reinterpret_cast<float4*>(p.q_rot_out + static_cast<size_t>(idx) * kHeadDim);
@@ -922,6 +970,10 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
           }
         }
         }
+        if (kScored && p.slopes) {
+          const int bh = __shfl_sync(kFull, cd_bh, t);
+          slope = g8 < G ? __ldg(p.slopes + (bh % p.hkv) * G + g8) * kLog2e : 0.f;
+        }
 #pragma unroll
         for (int d = 0; d < 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
         m_run = -INFINITY;
@@ -955,6 +1007,28 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
         // head g8, tokens 2tig, 2tig+1, 8+2tig, 9+2tig
         float sv[4] = {sc[0][0] + sc[0][2], sc[0][1] + sc[0][3], sc[1][0] + sc[1][2],
                        sc[1][1] + sc[1][3]};
+        const int seen = kScored ? __shfl_sync(kFull, cd_pos, t) : 0;
+        const int lo = seen % kPage;  // slots before it are not visible
+        if constexpr (kScored) {
+          if (p.cap > 0.f) {  // cap tanh(x) = cap - 2 cap / (e^2x + 1); the scores are 2 log2(e) x
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sv[k] = p.cap - 2.f * p.cap * fast_rcp(fast_exp2(sv[k]) + 1.f);
+          }
+          if (p.slopes) {
+            const float dist = static_cast<float>(seen / kPage - 2 * tig);  // of this lane's first slot
+            sv[0] -= slope * dist;
+            sv[1] -= slope * (dist - 1.f);
+            sv[2] -= slope * (dist - 8.f);
+            sv[3] -= slope * (dist - 9.f);
+          }
+          if (lo > 0) {
+            const int t0 = 2 * tig;
+            if (t0 < lo) sv[0] = -INFINITY;
+            if (t0 + 1 < lo) sv[1] = -INFINITY;
+            if (t0 + 8 < lo) sv[2] = -INFINITY;
+            if (t0 + 9 < lo) sv[3] = -INFINITY;
+          }
+        }
         if (nv < kPage) {
           const int t0 = 2 * tig;
           if (t0 >= nv) sv[0] = -INFINITY;
@@ -1007,6 +1081,16 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
             vb[d][1] &= m1;
           }
         }
+        if (kScored && lo > 0) {  // nor may the rows before the first visible slot reach the product
+          const int t0 = 2 * tig;
+          const uint32_t m0 = (t0 >= lo ? 0x0000ffffu : 0u) | (t0 + 1 >= lo ? 0xffff0000u : 0u);
+          const uint32_t m1 = (t0 + 8 >= lo ? 0x0000ffffu : 0u) | (t0 + 9 >= lo ? 0xffff0000u : 0u);
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            vb[d][0] &= m0;
+            vb[d][1] &= m1;
+          }
+        }
 #pragma unroll
         for (int d = 0; d < 8; ++d) mma_bf16_16816(o[d], ap, vb[d][0], vb[d][1]);
       }
@@ -1053,9 +1137,9 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
         } else if (complete) {
           if (live) {
             const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
-            float2* dst = reinterpret_cast<float2*>(p.out + (row0 + g8) * kHeadDim);
 #pragma unroll
-            for (int d = 0; d < 8; ++d) dst[4 * d + tig] = make_float2(of[d].x * inv, of[d].y * inv);
+            for (int d = 0; d < 8; ++d)
+              store_pair<kMode>(p, row0 + g8, 4 * d + tig, of[d].x * inv, of[d].y * inv);
           }
         } else if (first_in_range) {
           // A split piece that opens the range: its unnormalised accumulator,
@@ -1083,9 +1167,9 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
         const unsigned run = __ballot_sync(kFull, w2 < kW && s_first_bh[w2 < kW ? w2 : 0] == sg);
         const int k = __ffs(~run) - 1;
         fold_run<G>(pc, s_slots + (w + 1) * C::kSlotFloats, C::kSlotFloats, k, g8, tig);
-        float* out_row0 = p.out + static_cast<size_t>(sg) * G * kHeadDim;
+        const size_t row0 = static_cast<size_t>(sg) * G;
         if (g_first == g_last) {  // the whole segment lies in this group
-          store_output<G>(out_row0, pc, g8, tig);
+          store_output<G, kMode>(p, row0, pc, g8, tig);
           return;
         }
         // The CTA of the segment's last group merges it; the CTAs of its other
@@ -1123,7 +1207,7 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
           if (lane == 0) atomicOr(p.err, PKV_ERR_TIMEOUT);
           return;
         }
-        store_output<G>(out_row0, all, g8, tig);
+        store_output<G, kMode>(p, row0, all, g8, tig);
         for (int gg = g_first; gg < g_last; ++gg) {
           float* q = p.slots + static_cast<size_t>(2 * gg + (gg == g_first ? 1 : 0)) * C::kSlotFloats;
           for (int i = lane; i < C::kSlotFloats; i += 32) q[i] = 0.f;
@@ -1212,11 +1296,12 @@ struct Launcher {
   static Fn kernel(int mode) {
     return mode == kModePartials ? gqa_decode_kernel<G, kModePartials>
            : mode == kModeStep   ? gqa_decode_kernel<G, kModeStep>
+           : mode == kModeScored ? gqa_decode_kernel<G, kModeScored>
                                  : gqa_decode_kernel<G, kModeDecode>;
   }
 
   static int blocks_per_sm(int device, int mode) {
-    static std::atomic<int> cache[3][64];
+    static std::atomic<int> cache[4][64];
     const int d = device & 63;
     int v = cache[mode][d].load(std::memory_order_relaxed);
     if (v > 0) return v;
@@ -1374,7 +1459,7 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream) {
   const int group = a.num_q_heads / a.num_kv_heads;
   const bool partials = a.o_part != nullptr;
   const bool step = a.q_raw != nullptr;
-  const int mode = partials ? kModePartials : step ? kModeStep : kModeDecode;
+  const int mode = partials ? kModePartials : step ? kModeStep : a.scored ? kModeScored : kModeDecode;
   const int bps = blocks_per_sm_for(group, device, mode);
   if (bps < 1) return cudaErrorInvalidConfiguration;
   const int sms = device_sm_count(device);
@@ -1386,7 +1471,7 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream) {
   const int grid = decode_grid(group, device, mode);
   // the step's plan, for the automatic partition of a one-launch batch
   const long long warps = static_cast<long long>(sms) * bps * warps_per_cta(group);
-  const bool use_plan = !partials && a.pages_per_split == 0 && a.batch <= kDecodeBatchChunk &&
+  const bool use_plan = !partials && !a.scored && a.pages_per_split == 0 && a.batch <= kDecodeBatchChunk &&
                         a.workspace != nullptr;
   const int* plan = use_plan ? reinterpret_cast<const int*>(static_cast<const uint8_t*>(a.workspace) +
                                                             align256(slots_bytes(group, warps)))
@@ -1394,8 +1479,9 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream) {
   const int key = plan_key(a.num_kv_heads, group, grid, a.max_blocks * kPage,
                            step ? a.rope_positions : 0);
   const double log2e = 1.4426950408889634;
-  for (int b0 = 0; b0 < a.batch; b0 += kDecodeBatchChunk) {
-    const int nb = a.batch - b0 < kDecodeBatchChunk ? a.batch - b0 : kDecodeBatchChunk;
+  const int chunk = a.scored ? kScoredBatchChunk : kDecodeBatchChunk;
+  for (int b0 = 0; b0 < a.batch; b0 += chunk) {
+    const int nb = a.batch - b0 < chunk ? a.batch - b0 : chunk;
     DecodeParams p;
     p.num_pages = a.num_pages;
     p.hkv = a.num_kv_heads;
@@ -1434,6 +1520,15 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream) {
     p.rope_positions = a.rope_positions;
     p.q_rot_out = (step && a.q_rot_out) ? a.q_rot_out + qrow0 : nullptr;
     p.pool_w = const_cast<uint8_t*>(a.pool);
+    if (a.scored) {
+      p.out_bf16 = a.out_bf16;
+      if (a.out_bf16) p.out = reinterpret_cast<float*>(reinterpret_cast<uint16_t*>(a.out) + qrow0);
+      p.first_keys = a.first_keys ? a.first_keys + b0 : nullptr;
+      p.slopes = a.slopes;
+      p.window = a.window;
+      p.cap = static_cast<float>(static_cast<double>(a.softcap) * log2e);
+      if (a.softcap > 0.f) p.qscale = static_cast<float>(2.0 * static_cast<double>(a.scale) / a.softcap * log2e);
+    }
     e = launch_group(group, *a.kv_map, p, grid, stream, mode);
     if (e != cudaSuccess) return e;
   }

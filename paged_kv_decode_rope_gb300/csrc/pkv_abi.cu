@@ -40,6 +40,15 @@ bool decode_shape_ok(const pkv_pool_t* pool, int batch, int num_q_heads, int max
   return true;
 }
 
+// A scoring whose folded query scale is a finite fp32 number.
+bool scoring_ok(const pkv_scoring_t* s) {
+  if (!s || !std::isfinite(s->scale) || !std::isfinite(s->softcap) || s->softcap < 0.f || s->window < 0)
+    return false;
+  return s->softcap == 0.f || std::isfinite(3.f * s->scale / s->softcap);
+}
+
+bool out_type_ok(int type) { return type == PKV_BF16 || type == PKV_F32; }
+
 }  // namespace
 
 namespace pkv {
@@ -270,6 +279,21 @@ int paged_rope_table_build(double rope_theta, int num_positions, void* table, vo
   return e == cudaSuccess ? 0 : cuda_fail(e);
 }
 
+int paged_rope_table_build_freqs(const double* inv_freq, int num_freqs, double magnitude,
+                                 int num_positions, void* table, void* stream) {
+  if (!inv_freq || num_freqs < 1 || num_freqs > PKV_HEAD_DIM / 2 || !std::isfinite(magnitude) ||
+      num_positions < 1 || num_positions >= (1 << 24) || !table || !aligned16(table))
+    return -EINVAL;
+  double inv[PKV_HEAD_DIM / 2] = {};
+  for (int j = 0; j < num_freqs; ++j) {
+    if (!std::isfinite(inv_freq[j])) return -EINVAL;
+    inv[j] = inv_freq[j];
+  }
+  cudaError_t e = pkv::launch_rope_table(nullptr, num_positions, inv, magnitude, table,
+                                         static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? 0 : cuda_fail(e);
+}
+
 int paged_decode_step(pkv_pool_t* pool, const void* q, const void* k, const void* v,
                       const void* rope_table, int rope_positions, const int32_t* positions,
                       float* q_rot, float* out, const int32_t* block_tables, int max_blocks,
@@ -344,7 +368,7 @@ int paged_prefill(pkv_pool_t* pool, const void* q, const void* k, const void* v,
   const int sms = pkv::device_sm_count(device);
   const size_t need = paged_prefill_workspace_bytes(total_tokens, batch, max_blocks);
   if (sms < 1 || need == 0 || workspace_bytes < need) return -EINVAL;
-  pkv::PrefillLaunch a;
+  pkv::PrefillLaunch a = {};
   a.kv_map = &pool->kv_map;
   a.kv16_map = &pool->kv16_map;
   a.pool = static_cast<const uint8_t*>(pool->storage);
@@ -370,6 +394,94 @@ int paged_prefill(pkv_pool_t* pool, const void* q, const void* k, const void* v,
   a.sm_count = sms;
   a.err = pool->d_err;
   e = pkv::launch_prefill(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? 0 : cuda_fail(e);
+}
+
+int paged_gqa_decode_scored(const pkv_pool_t* pool, const float* q_rot, void* out, int out_type,
+                            const int32_t* block_tables, int max_blocks, const int32_t* seq_lens,
+                            const int32_t* first_keys, int batch, int num_q_heads,
+                            const pkv_scoring_t* scoring, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  if (!decode_shape_ok(pool, batch, num_q_heads, max_blocks) || max_blocks > (1 << 23) ||
+      !scoring_ok(scoring) || !out_type_ok(out_type))
+    return -EINVAL;
+  if (batch == 0) return 0;
+  if (!q_rot || !out || !block_tables || !seq_lens || !workspace) return -EINVAL;
+  if (!aligned16(q_rot) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return -EINVAL;
+  const size_t need = paged_gqa_decode_workspace_bytes(batch, num_q_heads, pool->num_kv_heads,
+                                                       max_blocks, 0);
+  if (need == 0 || workspace_bytes < need) return -EINVAL;
+  pkv::DecodeLaunch a = {};
+  a.kv_map = &pool->kv_map;
+  a.pool = static_cast<const uint8_t*>(pool->storage);
+  a.num_pages = pool->num_pages;
+  a.num_kv_heads = pool->num_kv_heads;
+  a.q_rot = q_rot;
+  a.out = static_cast<float*>(out);
+  a.block_tables = block_tables;
+  a.max_blocks = max_blocks;
+  a.seq_lens = seq_lens;
+  a.batch = batch;
+  a.num_q_heads = num_q_heads;
+  a.scale = scoring->scale;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  a.err = pool->d_err;
+  a.merge_looks = pool->merge_looks;
+  a.scored = true;
+  a.softcap = scoring->softcap;
+  a.slopes = scoring->alibi_slopes;
+  a.window = scoring->window;
+  a.first_keys = first_keys;
+  a.out_bf16 = out_type == PKV_BF16;
+  cudaError_t e = pkv::launch_decode(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? 0 : cuda_fail(e);
+}
+
+int paged_gqa_prefill_scored(const pkv_pool_t* pool, const float* q_rot, void* out, int out_type,
+                             const int32_t* block_tables, int max_blocks, const int32_t* cu_tokens,
+                             const int32_t* start_pos, const int32_t* prefix_lens,
+                             const int32_t* doc_starts, int batch, int total_tokens,
+                             int num_q_heads, const pkv_scoring_t* scoring, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (!decode_shape_ok(pool, total_tokens, num_q_heads, max_blocks) || batch < 0 || total_tokens < 0 ||
+      !scoring_ok(scoring) || !out_type_ok(out_type))
+    return -EINVAL;
+  if (total_tokens == 0) return 0;
+  if (batch < 1) return -EINVAL;
+  if (!q_rot || !out || !block_tables || !cu_tokens || !start_pos || !workspace) return -EINVAL;
+  if (!aligned16(q_rot) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return -EINVAL;
+  const size_t need = paged_prefill_workspace_bytes(total_tokens, batch, max_blocks);
+  if (need == 0 || workspace_bytes < need) return -EINVAL;
+  pkv::PrefillLaunch a = {};
+  a.kv_map = &pool->kv_map;
+  a.kv16_map = &pool->kv16_map;
+  a.pool = static_cast<const uint8_t*>(pool->storage);
+  a.num_pages = pool->num_pages;
+  a.num_kv_heads = pool->num_kv_heads;
+  a.q_rot = const_cast<float*>(q_rot);
+  a.out = static_cast<float*>(out);
+  a.block_tables = block_tables;
+  a.max_blocks = max_blocks;
+  a.cu_tokens = cu_tokens;
+  a.start_pos = start_pos;
+  a.batch = batch;
+  a.total_tokens = total_tokens;
+  a.num_q_heads = num_q_heads;
+  a.scale = scoring->scale;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  a.err = pool->d_err;
+  a.scored = true;
+  a.softcap = scoring->softcap;
+  a.slopes = scoring->alibi_slopes;
+  a.window = scoring->window;
+  a.prefix_lens = prefix_lens;
+  a.doc_starts = doc_starts;
+  a.out_bf16 = out_type == PKV_BF16;
+  cudaError_t e = pkv::launch_prefill(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? 0 : cuda_fail(e);
 }
 

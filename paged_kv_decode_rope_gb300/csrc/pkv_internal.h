@@ -85,6 +85,13 @@ struct DecodeLaunch {
   int rope_positions;
   const int32_t* positions;  // [batch] RoPE position of each new token
   float* q_rot_out;
+  // the scored decode (pkv_scoring): capped, biased, windowed scores
+  bool scored;
+  float softcap;              // 0: none
+  const float* slopes;        // [num_q_heads] or null
+  int window;                 // 0: none
+  const int32_t* first_keys;  // [batch] or null
+  int out_bf16;               // `out` holds bf16
 };
 
 // Chunked causal prefill (prefill.cu): every chunk token becomes a one-token
@@ -114,6 +121,14 @@ struct PrefillLaunch {
   size_t workspace_bytes;
   int sm_count;
   int* err;
+  // scored attention (pkv_scoring): q_rot is an input, nothing is appended
+  bool scored;
+  float softcap;               // 0: none
+  const float* slopes;         // [num_q_heads] or null
+  int window;                  // 0: none
+  const int32_t* prefix_lens;  // [batch] or null
+  const int32_t* doc_starts;   // [total_tokens] or null
+  int out_bf16;                // `out` holds bf16
 };
 
 size_t prefill_workspace_bytes(int total_tokens, int batch, int max_blocks);
@@ -139,6 +154,11 @@ cudaError_t launch_plan(const int32_t* seq_lens, const int32_t* positions, int r
 // positions is null.
 cudaError_t launch_rope_cos_sin(const int32_t* positions, int rows, double rope_theta,
                                 void* table, cudaStream_t stream);
+
+// The same table for 32 given inverse frequencies (host), its values
+// multiplied by magnitude.
+cudaError_t launch_rope_table(const int32_t* positions, int rows, const double* inv_freq, double magnitude,
+                              void* table, cudaStream_t stream);
 
 cudaError_t launch_split_combine(const float* o_part, const float* lse_part,
                                  const int32_t* num_splits, float* out, int rows, int max_splits,
