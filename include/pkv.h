@@ -467,10 +467,10 @@ int paged_rope_table_build_freqs(const double *inv_freq, int num_freqs, double m
  * dims (j, j + rot_dim/2), or (2j, 2j+1) when interleaved != 0; it is rotated
  * by entry j of the table row of the token's position. Dims from rot_dim on
  * are passed through.
- *   q, k, v    bf16 [tokens][heads][64], 8-byte aligned; token t's heads start
+ *   q, k, v    bf16 [tokens][heads][64], 16-byte aligned; token t's heads start
  *              at element t * q_stride (k_stride, v_stride), so that they may
  *              be slices of one projection's output. Strides are multiples
- *              of 4 elements, at least heads * 64.
+ *              of 8 elements, at least heads * 64.
  *   q_rot      fp32 [tokens][num_q_heads][64] out, 16-byte aligned
  *   slot_map   int32 [tokens], this layer's slots (paged_tables_build): page *
  *              16 + slot. A token with a negative slot is rotated, not stored.

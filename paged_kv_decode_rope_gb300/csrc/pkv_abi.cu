@@ -455,6 +455,11 @@ int paged_gqa_prefill_scored(const pkv_pool_t* pool, const float* q_rot, void* o
     return -EINVAL;
   const size_t need = paged_prefill_workspace_bytes(total_tokens, batch, max_blocks);
   if (need == 0 || workspace_bytes < need) return -EINVAL;
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return cuda_fail(e);
+  const int sms = pkv::device_sm_count(device);
+  if (sms < 1) return -EINVAL;
   pkv::PrefillLaunch a = {};
   a.kv_map = &pool->kv_map;
   a.kv16_map = &pool->kv16_map;
@@ -473,15 +478,15 @@ int paged_gqa_prefill_scored(const pkv_pool_t* pool, const float* q_rot, void* o
   a.scale = scoring->scale;
   a.workspace = workspace;
   a.workspace_bytes = workspace_bytes;
+  a.sm_count = sms;
   a.err = pool->d_err;
-  a.scored = true;
   a.softcap = scoring->softcap;
   a.slopes = scoring->alibi_slopes;
   a.window = scoring->window;
   a.prefix_lens = prefix_lens;
   a.doc_starts = doc_starts;
   a.out_bf16 = out_type == PKV_BF16;
-  cudaError_t e = pkv::launch_prefill(a, static_cast<cudaStream_t>(stream));
+  e = pkv::launch_prefill_scored(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? 0 : cuda_fail(e);
 }
 

@@ -121,8 +121,7 @@ struct PrefillLaunch {
   size_t workspace_bytes;
   int sm_count;
   int* err;
-  // scored attention (pkv_scoring): q_rot is an input, nothing is appended
-  bool scored;
+  // launch_prefill_scored (pkv_scoring): q_rot is an input, nothing is appended
   float softcap;               // 0: none
   const float* slopes;         // [num_q_heads] or null
   int window;                  // 0: none
@@ -133,6 +132,8 @@ struct PrefillLaunch {
 
 size_t prefill_workspace_bytes(int total_tokens, int batch, int max_blocks);
 cudaError_t launch_prefill(const PrefillLaunch& a, cudaStream_t stream);
+// The attention alone, with pkv_scoring scores; the same workspace.
+cudaError_t launch_prefill_scored(const PrefillLaunch& a, cudaStream_t stream);
 
 // Largest batch one decode launch serves (sequence lengths and page prefix sums
 // are staged in shared memory); larger batches are cut into several launches.

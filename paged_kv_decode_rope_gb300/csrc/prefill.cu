@@ -22,6 +22,7 @@
 #include <climits>
 #include <cub/block/block_scan.cuh>
 
+#include "f32x2.cuh"
 #include "pkv_device.cuh"
 #include "tc05.cuh"
 #include "pkv_internal.h"
@@ -271,15 +272,6 @@ struct PrefillAttnParams {
   long long num_pages;
   float qscale;  // scale * log2(e)
   int* err;
-  // scored attention (pkv_scoring)
-  const int32_t* cu_tokens;    // [batch + 1]
-  const int32_t* start_pos;    // [batch]
-  const int32_t* prefix_lens;  // [batch] or null
-  const int32_t* doc_starts;   // [T] or null
-  const float* slopes;         // [hq] or null
-  int window;                  // 0: none
-  float cap;                   // softcap * log2(e), 0: none (qscale then holds 2 log2(e) scale / softcap)
-  int out_bf16;
 };
 
 // ---------------------------------------------------------------------------
@@ -335,7 +327,6 @@ struct TcCfg {
   static constexpr uint32_t kBytes = kStage0 + kStages * 2 * kStep;
 };
 constexpr float kSlack = 8.f;
-constexpr float kLog2e = 1.4426950408889634f;
 // tensor memory: three S buffers in columns 0-63, 64-127 and 128-191 (step j
 // uses buffer j % 3), O in 192-255. Step j's P is written over its own S:
 // P_hi in the buffer's first 32 columns and P_lo in the next 32 (two bf16
@@ -345,88 +336,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kSBufs = 3;
 constexpr uint32_t kTmemCols = 256;
 
-// Two fp32 values in one 64-bit register, and the paired fp32 arithmetic of
-// sm_100 and later (each half rounded exactly as the scalar operation).
-__device__ __forceinline__ uint64_t f32x2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
-  float a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-  return make_float2(a, b);
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t sub_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-// Bounded wait for the copy and product warps, which are normally ahead of
-// the softmax: after a first test, they sleep between tests instead of
-// polling, so that their spinning does not take issue slots from the softmax
-// warps on the same sub-partition.
-__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    __nanosleep(32);
-    if (mbar_try_wait(bar, parity)) return true;
-  }
-  return false;
-}
-
-// p0 - h.lo and p1 - h.hi for the two bf16 halves of h, each in one
-// mixed-precision fma (bf16 times bf16 -1, plus fp32; sm_100 and later):
-// exact when h is p rounded to bf16, so the remainder of the split
-__device__ __forceinline__ float2 bf16x2_remainder(uint32_t h, float p0, float p1) {
-  float r0, r1;
-  asm("{\n\t.reg .b16 h0, h1, m1;\n\t"
-      "mov.b32 {h0, h1}, %2;\n\t"
-      "mov.b16 m1, 0xBF80;\n\t"
-      "fma.rn.f32.bf16 %0, h0, m1, %3;\n\t"
-      "fma.rn.f32.bf16 %1, h1, m1, %4;\n\t}"
-      : "=f"(r0), "=f"(r1)
-      : "r"(h), "f"(p0), "f"(p1));
-  return make_float2(r0, r1);
-}
-
-// Move registers between the warpgroups of a CTA (every warp of a warpgroup
-// executes the same instruction): dec gives back down to N a thread, inc
-// waits until N a thread are free.
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// max of three floats in one instruction (sm_100 and later)
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// Scored attention (kScored) runs the same steps with three differences. A row
-// sees the keys [lo, hi) that its window, document and prefix leave it, so the
-// tile's steps run from the page that holds the smallest lo of its rows to
-// its largest hi; positions count from there (key0; pages before it are not
-// looked up), and only the steps at the rows' own ends mask. Scores are capped (cap - 2 cap / (e^2x + 1), with
-// 2 log2(e) / softcap in the query's scale) and biased on their way out of
-// tensor memory. The output is fp32 or bf16.
-template <int G, bool kScored>
+template <int G>
 __global__ void __launch_bounds__(TcCfg<G>::kThreads, 2)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap kv16_map, const PrefillAttnParams p) {
   using C = TcCfg<G>;
@@ -439,66 +349,22 @@ __global__ void __launch_bounds__(TcCfg<G>::kThreads, 2)
   // CTA x works on tile x / hkv for kv head x % hkv: the hardware hands CTAs
   // out in order of x, so the order of the tiles (most steps first) holds
   // across all kv heads
-  if constexpr (kScored) grid_dependency_wait();  // the tile plan is the kernel before this one
   const int ti = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.hkv));
   const int h = static_cast<int>(blockIdx.x - static_cast<unsigned>(ti) * static_cast<unsigned>(p.hkv));
   if (ti >= *p.num_tiles) return;
   const int4 tile = p.tiles[ti];
-  const int b = tile.x, row0 = tile.y, n_tok = tile.z;
-  int pos0 = tile.w;
+  const int b = tile.x, row0 = tile.y, n_tok = tile.z, pos0 = tile.w;
   const long long room = p.pos_cap - pos0;
-  int n_ok = pos0 < 0 ? 0 : static_cast<int>(min(static_cast<long long>(n_tok), max(room, 0ll)));
-  // scored: keys past the chunk's end exist for no query; a prefix reaches up to it
-  int key0 = 0, end = 0, lo_tile = 0;
-  [[maybe_unused]] auto first_key = [&](int t) {  // of the tile's token t
-    int lo = p.doc_starts ? max(p.doc_starts[row0 + t], 0) : 0;
-    if (p.window > 0) lo = max(lo, tile.w + t - p.window + 1);
-    return lo;
-  };
-  [[maybe_unused]] auto last_key = [&](int t) { return max(tile.w + t, end - 1); };
-  if constexpr (kScored) {
-    const int start = p.start_pos[b];
-    if (start < 0) n_ok = 0;
-    if (n_ok < n_tok && tid == 0) atomicOr(p.err, PKV_ERR_SEQ_LEN);
-    __shared__ int s_lo;
-    if (tid == 0) s_lo = INT_MAX;
-    __syncthreads();
-    if (n_ok > 0) {
-      if (p.prefix_lens) {  // keys below `end` are seen by every query of the sequence
-        const long long len = static_cast<long long>(start) + (p.cu_tokens[b + 1] - p.cu_tokens[b]);
-        end = static_cast<int>(min(static_cast<long long>(max(p.prefix_lens[b], 0)), min(len, p.pos_cap)));
-      }
-      if (tid < n_ok) {
-        const int lo = first_key(tid);
-        if (lo <= last_key(tid)) atomicMin(&s_lo, lo);
-      }
-    }
-    __syncthreads();
-    if (s_lo == INT_MAX) {
-      n_ok = 0;  // no row sees a key
-    } else {
-      key0 = s_lo / kPage * kPage;
-      lo_tile = s_lo - key0;
-      pos0 -= key0;
-      end -= key0;
-    }
-    // rows past n_ok, all of them when no row sees a key
-    const int words = G * kHeadDim / (p.out_bf16 ? 2 : 1);
-    for (int e = n_ok * words + tid; e < n_tok * words; e += C::kThreads) {
-      const int t = e / words, rest = e - t * words;
-      reinterpret_cast<uint32_t*>(p.out)[static_cast<size_t>(row0 + t) * (p.hq / G) * words + h * words + rest] = 0u;
-    }
-  } else {
-    for (int e = n_ok * G * kHeadDim + tid; e < n_tok * G * kHeadDim; e += C::kThreads) {
-      const int t = e / (G * kHeadDim), rest = e - t * (G * kHeadDim);
-      p.out[(static_cast<size_t>(row0 + t) * p.hq + h * G) * kHeadDim + rest] = 0.f;
-    }
+  const int n_ok = pos0 < 0 ? 0 : static_cast<int>(min(static_cast<long long>(n_tok), max(room, 0ll)));
+  for (int e = n_ok * G * kHeadDim + tid; e < n_tok * G * kHeadDim; e += C::kThreads) {
+    const int t = e / (G * kHeadDim), rest = e - t * (G * kHeadDim);
+    p.out[(static_cast<size_t>(row0 + t) * p.hq + h * G) * kHeadDim + rest] = 0.f;
   }
   if (n_ok <= 0) return;
-  const int last_pos = kScored ? max(pos0 + n_ok, end) - 1 : pos0 + n_ok - 1;
+  const int last_pos = pos0 + n_ok - 1;
   const int n_pages = last_pos / kPage + 1;
   const int n_steps = (n_pages + 3) / 4;
-  const int32_t* bt = p.block_tables + static_cast<size_t>(b) * p.max_blocks + key0 / kPage;
+  const int32_t* bt = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
   const uint32_t base = (smem_addr(dsmem) + 1023u) & ~1023u;
   uint8_t* gbase = dsmem + (base - smem_addr(dsmem));
   auto kst = [&](int st) { return base + C::kStage0 + st * 2 * C::kStep; };
@@ -682,19 +548,6 @@ __global__ void __launch_bounds__(TcCfg<G>::kThreads, 2)
       live[hh] = rw < C::kRows && tok[hh] < n_ok;
       pos[hh] = pos0 + min(tok[hh], n_ok - 1);
     }
-    // scored: the keys each row sees, its slope (base 2), and the steps
-    // between which neither row masks
-    int lo[2] = {0, 0}, hi[2] = {pos[0], pos[1]};  // [lo, hi], hi included
-    float slope[2] = {0.f, 0.f};
-    if constexpr (kScored) {
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        lo[hh] = first_key(min(tok[hh], n_ok - 1)) - key0;
-        hi[hh] = max(pos[hh], end - 1);
-        if (p.slopes) slope[hh] = p.slopes[h * G + gix[hh]] * kLog2e;
-      }
-    }
-    const int free0 = max(lo[0], lo[1]), free1 = min(hi[0], hi[1]);
     // Q rows: scaled, as bf16 high part and remainder, 128-byte swizzled
     // (this thread: dims 16 q .. 16 q + 15 of its two rows, chunks 2 q and 2 q + 1)
 #pragma unroll
@@ -756,34 +609,7 @@ __global__ void __launch_bounds__(TcCfg<G>::kThreads, 2)
       auto load_s = [&]() {
         tmem_ld_16x256b_x8(tS(j) + lane_addr, sv);
         tmem_wait_ld();
-        if constexpr (kScored) {
-          if (p.cap > 0.f) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) sv[i] = p.cap - 2.f * p.cap * fast_rcp(fast_exp2(sv[i]) + 1.f);
-          }
-          if (p.slopes) {
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const float d0 = static_cast<float>(kb - pos[hh]);  // of the first key from the query
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  sv[4 * i + 2 * hh + e] -= slope[hh] * fabsf(d0 + static_cast<float>(8 * i + e));
-            }
-          }
-          if (64 * j < free0 || 64 * j + 63 > free1 || bad) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int key = kb + 8 * i + e;
-                  if (key < lo[hh] || key > hi[hh] || ((bad >> (i >> 1)) & 1)) sv[4 * i + 2 * hh + e] = -INFINITY;
-                }
-          }
-        } else if (64 * j + 63 > pos[0] || bad) {
+        if (64 * j + 63 > pos[0] || bad) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -903,12 +729,12 @@ __global__ void __launch_bounds__(TcCfg<G>::kThreads, 2)
       // V rows that hold no key of the tile (past its last position, or of a
       // page with a bad id) are zeroed once the stage's V copies have landed,
       // so that their bits cannot reach O
-      if (64 * j + 63 > last_pos || bad || (kScored && 64 * j < lo_tile)) {
+      if (64 * j + 63 > last_pos || bad) {
         if (!mbar_wait_bounded(smem_addr(&v_full[st]), (j / C::kStages) & 1)) failed = true;
         uint8_t* vrow = gbase + (vst(st) - base);
         for (int idx = tid; idx < 64 * 8; idx += C::kSoftmaxThreads) {
           const int key = idx >> 3;
-          if (64 * j + key > last_pos || ((bad >> (key >> 4)) & 1) || (kScored && 64 * j + key < lo_tile))
+          if (64 * j + key > last_pos || ((bad >> (key >> 4)) & 1))
             *reinterpret_cast<uint4*>(vrow + key * 128 + (idx & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();  // the zeroed rows, before the tensor core reads V
@@ -934,17 +760,7 @@ __global__ void __launch_bounds__(TcCfg<G>::kThreads, 2)
         l += __shfl_xor_sync(kFull, l, 2);
         if (live[hh]) {
           const float inv = l > 0.f ? 1.f / l : 0.f;
-          const size_t at = (static_cast<size_t>(row0 + tok[hh]) * p.hq + h * G + gix[hh]) * kHeadDim + 2 * q;
-          if constexpr (kScored) {
-            if (p.out_bf16) {
-              uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + at);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[4 * i] = pack_bf16x2(o[4 * i + 2 * hh] * inv, o[4 * i + 2 * hh + 1] * inv);
-              continue;
-            }
-          }
-          float* dst = p.out + at;
+          float* dst = p.out + (static_cast<size_t>(row0 + tok[hh]) * p.hq + h * G + gix[hh]) * kHeadDim + 2 * q;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             *reinterpret_cast<float2*>(dst + 8 * i) =
@@ -989,31 +805,9 @@ PrefillLayout layout(int total_tokens, int batch, int max_blocks) {
   return l;
 }
 
-// The attention kernel's one-time setup: its shared memory, and the check that
-// the warpgroups' register shares fit in what the launch gives the CTA (the
-// compiler's count a thread x its threads): otherwise the softmax warps'
-// increase would wait for registers that never come, so the call is refused.
-template <int G, bool kScored>
-cudaError_t configure_attention(int smem) {
-  using C = TcCfg<G>;
-  static std::atomic<bool> done;
-  if (done.load(std::memory_order_relaxed)) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<G, kScored>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, prefill_tc_kernel<G, kScored>);
-  if (e != cudaSuccess) return e;
-  if (128 * C::kIssueRegs + C::kSoftmaxThreads * C::kSoftmaxRegs > C::kThreads * fa.numRegs)
-    return cudaErrorInvalidConfiguration;
-  done.store(true, std::memory_order_relaxed);
-  return cudaSuccess;
-}
-
-// The launches of a prefill call for groups of G query heads: the preparation
-// (token expansion and tile plan), the append, the attention; a scored
-// attention call, whose keys are already in the pool, has the tile plan and
-// the attention only.
-template <int G, bool kScored>
+// The three launches of a prefill call for groups of G query heads: the
+// preparation (token expansion and tile plan), the append, the attention.
+template <int G>
 cudaError_t launch_all(const PrefillLaunch& a, const PrefillLayout& l, cudaStream_t stream) {
   using C = TcCfg<G>;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
@@ -1022,31 +816,30 @@ cudaError_t launch_all(const PrefillLaunch& a, const PrefillLayout& l, cudaStrea
   int4* tiles = reinterpret_cast<int4*>(ws + l.tiles);
   int* count = reinterpret_cast<int*>(ws + l.count);
   const size_t grid_x = static_cast<size_t>(a.total_tokens + C::kTokens - 1) / C::kTokens + a.batch;
-  const int expand_blocks = kScored ? 0 : (a.total_tokens + kPlanThreads - 1) / kPlanThreads;
+  const int expand_blocks = (a.total_tokens + kPlanThreads - 1) / kPlanThreads;
   prefill_prep_kernel<<<1 + expand_blocks, kPlanThreads, 0, stream>>>(
       a.max_blocks, a.rope_positions, a.cu_tokens, a.start_pos, a.batch, a.total_tokens, tok_seq,
       tok_pos, C::kTokens, static_cast<int>(grid_x), tiles, count, a.err);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  PrefillAttnParams p = {};
-  p.pos_cap = static_cast<long long>(a.max_blocks) * kPage;
-  if constexpr (!kScored) {
-    // the caller's RoPE table: fp32 pair rows, then fp64 rows, one per position
-    const float4* rope_ff = static_cast<const float4*>(a.rope_table);
-    const double2* rope_dd =
-        reinterpret_cast<const double2*>(rope_ff + static_cast<size_t>(a.rope_positions) * kHalfDim);
-    prefill_append_kernel<<<a.total_tokens, kAppendThreads, 0, stream>>>(
-        const_cast<uint16_t*>(reinterpret_cast<const uint16_t*>(a.pool)), a.num_pages, a.num_kv_heads,
-        a.num_q_heads, a.q, a.k, a.v, a.q_rot, a.block_tables, a.max_blocks, tok_seq, tok_pos, rope_ff,
-        rope_dd, a.err);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    if (a.rope_positions < p.pos_cap) p.pos_cap = a.rope_positions;
-  }
+  // the caller's RoPE table: fp32 pair rows, then fp64 rows, one per position
+  const float4* rope_ff = static_cast<const float4*>(a.rope_table);
+  const double2* rope_dd =
+      reinterpret_cast<const double2*>(rope_ff + static_cast<size_t>(a.rope_positions) * kHalfDim);
+  prefill_append_kernel<<<a.total_tokens, kAppendThreads, 0, stream>>>(
+      const_cast<uint16_t*>(reinterpret_cast<const uint16_t*>(a.pool)), a.num_pages, a.num_kv_heads,
+      a.num_q_heads, a.q, a.k, a.v, a.q_rot, a.block_tables, a.max_blocks, tok_seq, tok_pos, rope_ff,
+      rope_dd, a.err);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  PrefillAttnParams p;
   p.q_rot = a.q_rot;
   p.out = a.out;
   p.block_tables = a.block_tables;
   p.max_blocks = a.max_blocks;
+  p.pos_cap = static_cast<long long>(a.max_blocks) * kPage < a.rope_positions
+                  ? static_cast<long long>(a.max_blocks) * kPage
+                  : static_cast<long long>(a.rope_positions);
   p.tiles = tiles;
   p.num_tiles = count;
   p.hkv = a.num_kv_heads;
@@ -1054,21 +847,21 @@ cudaError_t launch_all(const PrefillLaunch& a, const PrefillLayout& l, cudaStrea
   p.num_pages = a.num_pages;
   p.qscale = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.err = a.err;
-  if constexpr (kScored) {
-    p.cu_tokens = a.cu_tokens;
-    p.start_pos = a.start_pos;
-    p.prefix_lens = a.prefix_lens;
-    p.doc_starts = a.doc_starts;
-    p.slopes = a.slopes;
-    p.window = a.window;
-    p.cap = static_cast<float>(static_cast<double>(a.softcap) * 1.4426950408889634);
-    if (a.softcap > 0.f)
-      p.qscale = static_cast<float>(2.0 * static_cast<double>(a.scale) / a.softcap * 1.4426950408889634);
-    p.out_bf16 = a.out_bf16;
-  }
   const int smem = static_cast<int>(C::kBytes + 1024);  // + alignment to 1 KiB
-  e = configure_attention<G, kScored>(smem);
-  if (e != cudaSuccess) return e;
+  static std::atomic<bool> attr_set[9];
+  if (!attr_set[G].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(prefill_tc_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    // The warpgroups' register shares must fit in what the launch gives the
+    // CTA (the compiler's count a thread x its threads), or the softmax
+    // warps' increase would wait for registers that never come: refuse.
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, prefill_tc_kernel<G>);
+    if (e != cudaSuccess) return e;
+    if (128 * C::kIssueRegs + C::kSoftmaxThreads * C::kSoftmaxRegs > C::kThreads * fa.numRegs)
+      return cudaErrorInvalidConfiguration;
+    attr_set[G].store(true, std::memory_order_relaxed);
+  }
   const size_t n_ctas = grid_x * static_cast<size_t>(a.num_kv_heads);
   if (n_ctas > 0x7fffffffu) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(n_ctas));
@@ -1083,12 +876,7 @@ cudaError_t launch_all(const PrefillLaunch& a, const PrefillLayout& l, cudaStrea
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<G, kScored>, *a.kv16_map, p);
-}
-
-template <int G>
-cudaError_t launch_group(const PrefillLaunch& a, const PrefillLayout& l, cudaStream_t stream) {
-  return a.scored ? launch_all<G, true>(a, l, stream) : launch_all<G, false>(a, l, stream);
+  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<G>, *a.kv16_map, p);
 }
 
 }  // namespace
@@ -1102,14 +890,14 @@ cudaError_t launch_prefill(const PrefillLaunch& a, cudaStream_t stream) {
   const PrefillLayout l = layout(a.total_tokens, a.batch, a.max_blocks);
 
   switch (a.num_q_heads / a.num_kv_heads) {
-    case 1: return launch_group<1>(a, l, stream);
-    case 2: return launch_group<2>(a, l, stream);
-    case 3: return launch_group<3>(a, l, stream);
-    case 4: return launch_group<4>(a, l, stream);
-    case 5: return launch_group<5>(a, l, stream);
-    case 6: return launch_group<6>(a, l, stream);
-    case 7: return launch_group<7>(a, l, stream);
-    case 8: return launch_group<8>(a, l, stream);
+    case 1: return launch_all<1>(a, l, stream);
+    case 2: return launch_all<2>(a, l, stream);
+    case 3: return launch_all<3>(a, l, stream);
+    case 4: return launch_all<4>(a, l, stream);
+    case 5: return launch_all<5>(a, l, stream);
+    case 6: return launch_all<6>(a, l, stream);
+    case 7: return launch_all<7>(a, l, stream);
+    case 8: return launch_all<8>(a, l, stream);
     default: return cudaErrorInvalidValue;
   }
 }

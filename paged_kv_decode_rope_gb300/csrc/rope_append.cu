@@ -10,15 +10,20 @@
 // where it cannot), as every other append of this library; v is copied.
 //
 // The kernel moves (Hq + 2 Hkv) * 128 bytes in and Hq * 256 + Hkv * 256 out a
-// token and computes next to nothing, so memory bounds it. One CTA a token:
-// 16 threads hold a head's row, 4 dims (8 bytes of bf16, 16 of fp32) each, so
-// that every access is a full row in one go; a thread keeps the same 4 dims of
-// every row it takes and therefore reads its cos and sin once. The rotated
-// partner of a dim is in the same thread (interleaved) or in another of the
-// same 16 (half pairs: rot_dim is a multiple of 8, so partners come in whole
-// 4-dim pieces), reached by a shuffle. kRows rows a thread are loaded before
-// the first is used, ahead of the position -> table row chain.
+// token and computes next to nothing, so memory bounds it, and what it takes
+// is bytes in flight: the cos and sin of a token depend on its position, and a
+// CTA a token spent its life waiting for that chain (48 us for 8192 tokens of
+// 32 + 8 heads, 42% of the copy bandwidth). So CTAs stay and stream units (a
+// token, up to kUnitRows of its rows) through a ring of kStages shared-memory
+// stages: one warp reads positions and slots ahead and issues bulk copies of
+// the unit's rows and its table row; kRopeWarps warps rotate and store. 16
+// threads hold a head's row, 4 dims (8 bytes of bf16, 16 of fp32) each, so every
+// access is a full row in one go; a thread keeps the same 4 dims of every row.
+// The rotated partner of a dim is in the same thread (interleaved) or in
+// another of the same 16 (half pairs: rot_dim is a multiple of 8, so partners
+// come in whole 4-dim pieces), reached by a shuffle. Every wait is bounded.
 #include <cerrno>
+#include <initializer_list>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -27,9 +32,14 @@ namespace pkv {
 namespace {
 
 constexpr int kHalfDim = kHeadDim / 2;
-constexpr int kPieces = kHeadDim / 4;  // threads a row
-constexpr int kRopeThreads = 256;
-constexpr int kRows = 4;               // rows a thread loads at once
+constexpr int kPieces = kHeadDim / 4;          // threads a row
+constexpr int kRopeWarps = 8;                  // consumers
+constexpr int kRopeThreads = 32 * (kRopeWarps + 1);
+constexpr int kUnitRows = 64;                  // rows of a unit at most
+constexpr int kRopeStages = 4;
+constexpr int kTrigBytes = kHalfDim * 16;      // a row of the table's fp32 pairs
+constexpr int kStageBytes = kUnitRows * kRowBytes + kTrigBytes;
+constexpr int kRopeCtas = 3;                   // CTAs a SM
 
 struct RopeAppendParams {
   uint16_t* pool;
@@ -44,6 +54,8 @@ struct RopeAppendParams {
   const double2* rope_dd;  // [rows][32] {cos, sin}
   int rope_positions;
   int rot_dim;
+  int tokens;
+  int unit_rows, units;  // rows of a unit; units a token
   int* err;
 };
 
@@ -56,100 +68,167 @@ __device__ __noinline__ uint16_t rotate_key_dim(float x, float xp, const double2
 }
 
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeAppendParams p) {
-  const int tkn = blockIdx.x, tid = threadIdx.x;
-  const int piece = tid % kPieces;                     // this thread's dims: 4 piece .. + 3
-  const int step = blockDim.x / kPieces;               // rows a pass of the CTA
-  const int rows = p.hq + 2 * p.hkv;                   // q heads, then k heads, then v heads
-  const int half = p.rot_dim / 2;
-  const bool turns = 4 * piece < p.rot_dim;
-  // half pairs: the piece that holds this one's partners, on which side this one is
-  const bool upper = !kInterleaved && 4 * piece >= half;
-  const int partner = !turns ? piece : upper ? piece - half / 4 : piece + half / 4;
-
-  auto load = [&](int row) {
-    if (row >= rows) return make_uint2(0u, 0u);
-    const uint16_t* src = row < p.hq ? p.q + tkn * p.q_stride + row * kHeadDim
-                          : row < p.hq + p.hkv ? p.k + tkn * p.k_stride + (row - p.hq) * kHeadDim
-                                               : p.v + tkn * p.v_stride + (row - p.hq - p.hkv) * kHeadDim;
-    return __ldg(reinterpret_cast<const uint2*>(src + 4 * piece));
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(const RopeAppendParams p) {
+  extern __shared__ __align__(128) uint8_t s_ring[];
+  __shared__ __align__(8) uint64_t full[kRopeStages], empty[kRopeStages];
+  __shared__ int2 s_token[kRopeStages];  // position (-1: none in the table) and slot (-1: not stored)
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rows = p.hq + 2 * p.hkv;  // q heads, then k heads, then v heads
+  // unit i of this CTA: part `part` of token t, in steps of the grid
+  const int t_step = gridDim.x / p.units, part_step = gridDim.x % p.units;
+  int t = blockIdx.x / p.units, part = blockIdx.x % p.units;
+  auto next_unit = [&]() {
+    t += t_step;
+    part += part_step;
+    if (part >= p.units) {
+      part -= p.units;
+      ++t;
+    }
   };
-  uint2 x[kRows];
-  int row0 = tid / kPieces;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) x[i] = load(row0 + i * step);
-
-  const int pos = p.positions[tkn];
-  const int slot = p.slot_map[tkn];
-  const bool in_table = pos >= 0 && pos < p.rope_positions;
-  bool stores = in_table && slot >= 0;
-  if (stores && slot / kPage >= p.num_pages) {
-    stores = false;
-    if (tid == 0) atomicOr(p.err, PKV_ERR_PAGE_ID);
-  }
-  if (!in_table && tid == 0) atomicOr(p.err, PKV_ERR_POSITION);
-  // cos and sin of the thread's dims: entry j of dim e (hi and lo of each)
-  float4 cs[4];
-  const int j0 = kInterleaved ? 2 * piece : upper ? 4 * piece - half : 4 * piece;
-  const size_t at = static_cast<size_t>(in_table ? pos : 0) * kHalfDim + j0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) cs[e] = make_float4(1.f, 0.f, 0.f, 0.f);
-  if (turns) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) cs[e] = __ldg(p.rope_ff + at + (kInterleaved ? e / 2 : e));
-  }
-  uint16_t* page_base = p.pool + (stores ? static_cast<size_t>(slot / kPage) : 0) * p.hkv * (kHeadPageBytes / 2) +
-                        (slot & (kPage - 1)) * kHeadDim + 4 * piece;
-  const int lane0 = (tid & 31) & ~(kPieces - 1);
-
-  for (; row0 - tid / kPieces < rows; row0 += kRows * step) {  // the same trip count in all threads
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int row = row0 + i * step;
-      const uint2 w = x[i];
-      x[i] = load(row + kRows * step);
-      float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
-      const float own[4] = {a.x, a.y, b.x, b.y};
-      float other[4];  // what each dim's sin multiplies, with its sign: y = own cos - other sin
-      if (kInterleaved) {
-        other[0] = own[1];
-        other[1] = -own[0];
-        other[2] = own[3];
-        other[3] = -own[2];
-      } else {
-        a = bf16x2_to_float2(__shfl_sync(kFull, w.x, lane0 + partner));
-        b = bf16x2_to_float2(__shfl_sync(kFull, w.y, lane0 + partner));
-        other[0] = upper ? -a.x : a.x;
-        other[1] = upper ? -a.y : a.y;
-        other[2] = upper ? -b.x : b.x;
-        other[3] = upper ? -b.y : b.y;
-      }
-      if (row >= rows) continue;
-      if (row < p.hq) {
-        float y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[e] = turns ? own[e] * cs[e].x - other[e] * cs[e].z : own[e];
-          if (!in_table) y[e] = 0.f;
-        }
-        *reinterpret_cast<float4*>(p.q_rot + (static_cast<size_t>(tkn) * p.hq + row) * kHeadDim + 4 * piece) =
-            make_float4(y[0], y[1], y[2], y[3]);
-      } else if (stores) {
-        const bool key = row < p.hq + p.hkv;
-        const int h = row - p.hq - (key ? 0 : p.hkv);
-        uint2 out = w;
-        if (key && turns) {
-          uint16_t y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (!rotated_bf16_fast(own[e], other[e], cs[e].x, cs[e].y, cs[e].z, cs[e].w, y[e]))
-              y[e] = rotate_key_dim(own[e], other[e], p.rope_dd + at + (kInterleaved ? e / 2 : e));
-          out = make_uint2(y[0] | static_cast<uint32_t>(y[1]) << 16, y[2] | static_cast<uint32_t>(y[3]) << 16);
-        }
-        *reinterpret_cast<uint2*>(page_base + (h * 2 + (key ? 0 : 1)) * (kHalfBytes / 2)) = out;
-      }
+  if (tid == 0) {
+    for (int s = 0; s < kRopeStages; ++s) {
+      mbar_init(smem_addr(&full[s]), 1);
+      mbar_init(smem_addr(&empty[s]), kRopeWarps);
     }
   }
+  fence_mbar_init();
+  __syncthreads();
+  bool failed = false;
+
+  if (warp == kRopeWarps) {
+    // ---- the producer: lane 0 issues; positions and slots are read 32 units
+    // ahead, a unit a lane ----
+    int pos = 0, slot = 0;
+    int i = 0;
+    for (; t < p.tokens; next_unit(), ++i) {
+      const int st = i % kRopeStages, use = i / kRopeStages;
+      if (i % 32 == 0) {
+        const long long mine = t + (part + static_cast<long long>(lane) * gridDim.x) / p.units;
+        if (mine < p.tokens) {
+          pos = p.positions[mine];
+          slot = p.slot_map[mine];
+          int bits = 0;
+          if (pos < 0 || pos >= p.rope_positions) {
+            bits |= PKV_ERR_POSITION;
+            pos = slot = -1;
+          }
+          if (slot >= 0 && slot / kPage >= p.num_pages) {
+            bits |= PKV_ERR_PAGE_ID;
+            slot = -1;
+          }
+          if (bits) atomicOr(p.err, bits);
+        }
+      }
+      const int ps = __shfl_sync(kFull, pos, i % 32), sl = __shfl_sync(kFull, slot, i % 32);
+      if (use > 0 && !mbar_wait_bounded(smem_addr(&empty[st]), (use - 1) & 1)) failed = true;
+      if (__any_sync(kFull, failed)) {
+        failed = true;
+        break;
+      }
+      if (lane == 0) {
+        const int r0 = part * p.unit_rows;
+        const int r1 = min(r0 + p.unit_rows, rows);
+        const uint32_t bar = smem_addr(&full[st]), dst = smem_addr(s_ring) + st * kStageBytes;
+        s_token[st] = make_int2(ps, sl);
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>((r1 - r0) * kRowBytes + kTrigBytes));
+        bulk_g2s(dst + kUnitRows * kRowBytes, p.rope_ff + static_cast<size_t>(max(ps, 0)) * kHalfDim, kTrigBytes, bar);
+        auto copy = [&](const uint16_t* src, int first, int last) {  // rows first .. last - 1 of the unit's q, k or v
+          const int a = max(r0, first), b = min(r1, last);
+          if (a < b)
+            bulk_g2s(dst + (a - r0) * kRowBytes, src + static_cast<size_t>(a - first) * kHeadDim,
+                     static_cast<uint32_t>((b - a) * kRowBytes), bar);
+        };
+        copy(p.q + t * p.q_stride, 0, p.hq);
+        copy(p.k + t * p.k_stride, p.hq, p.hq + p.hkv);
+        copy(p.v + t * p.v_stride, p.hq + p.hkv, rows);
+      }
+      __syncwarp();
+    }
+    // let the copies still in flight land before shared memory goes away
+    if (failed && lane == 0)
+      for (int k = max(0, i - kRopeStages); k < i; ++k)
+        mbar_wait_bounded(smem_addr(&full[k % kRopeStages]), (k / kRopeStages) & 1);
+  } else {
+    // ---- the consumers ----
+    const int piece = tid % kPieces;  // this thread's dims: 4 piece .. + 3
+    const int half = p.rot_dim / 2;
+    const bool turns = 4 * piece < p.rot_dim;
+    // half pairs: the piece that holds this one's partners, on which side this one is
+    const bool upper = !kInterleaved && 4 * piece >= half;
+    const int partner = (lane & ~(kPieces - 1)) + (!turns ? piece : upper ? piece - half / 4 : piece + half / 4);
+    const int j0 = kInterleaved ? 2 * piece : upper ? 4 * piece - half : 4 * piece;  // its first entry of the table row
+    int i = 0;
+    for (; t < p.tokens; next_unit(), ++i) {
+      const int st = i % kRopeStages;
+      if (!mbar_wait_bounded(smem_addr(&full[st]), (i / kRopeStages) & 1)) failed = true;
+      if (__any_sync(kFull, failed)) {
+        failed = true;
+        break;
+      }
+      const int r0 = part * p.unit_rows;
+      const int n = min(p.unit_rows, rows - r0);
+      const uint32_t src = smem_addr(s_ring) + st * kStageBytes;
+      const int2 token = s_token[st];
+      float4 cs[4];  // {cos_hi, cos_lo, sin_hi, sin_lo} of each of the thread's dims
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        cs[e] = turns ? lds128f(src + kUnitRows * kRowBytes + 16 * (j0 + (kInterleaved ? e / 2 : e)))
+                      : make_float4(1.f, 0.f, 0.f, 0.f);
+      uint16_t* page = p.pool +
+                       static_cast<size_t>(max(token.y, 0) / kPage) * p.hkv * (kHeadPageBytes / 2) +
+                       (max(token.y, 0) % kPage) * kHeadDim + 4 * piece;
+      // two rows a warp; the warps take turns, so that the key rows, ten times
+      // the work of the others, do not always fall to the same ones
+      for (int r = 2 * ((warp + 4 * i) % kRopeWarps); r < n; r += 2 * kRopeWarps) {
+        const int local = r + lane / kPieces, row = r0 + local;
+        const uint2 w = lds64u(src + min(local, n - 1) * kRowBytes + 8 * piece);
+        float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
+        const float own[4] = {a.x, a.y, b.x, b.y};
+        float other[4];  // what each dim's sin multiplies, with its sign: y = own cos - other sin
+        if (kInterleaved) {
+          other[0] = own[1];
+          other[1] = -own[0];
+          other[2] = own[3];
+          other[3] = -own[2];
+        } else {
+          a = bf16x2_to_float2(__shfl_sync(kFull, w.x, partner));
+          b = bf16x2_to_float2(__shfl_sync(kFull, w.y, partner));
+          other[0] = upper ? -a.x : a.x;
+          other[1] = upper ? -a.y : a.y;
+          other[2] = upper ? -b.x : b.x;
+          other[3] = upper ? -b.y : b.y;
+        }
+        if (local >= n) continue;
+        if (row < p.hq) {
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[e] = turns ? own[e] * cs[e].x - other[e] * cs[e].z : own[e];
+            if (token.x < 0) y[e] = 0.f;
+          }
+          *reinterpret_cast<float4*>(p.q_rot + (static_cast<size_t>(t) * p.hq + row) * kHeadDim + 4 * piece) =
+              make_float4(y[0], y[1], y[2], y[3]);
+        } else if (token.y >= 0) {
+          const bool key = row < p.hq + p.hkv;
+          const int h = row - p.hq - (key ? 0 : p.hkv);
+          uint2 out = w;
+          if (key && turns) {
+            uint16_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!rotated_bf16_fast(own[e], other[e], cs[e].x, cs[e].y, cs[e].z, cs[e].w, y[e]))
+                y[e] = rotate_key_dim(own[e], other[e],
+                                      p.rope_dd + static_cast<size_t>(token.x) * kHalfDim + j0 + (kInterleaved ? e / 2 : e));
+            out = make_uint2(y[0] | static_cast<uint32_t>(y[1]) << 16, y[2] | static_cast<uint32_t>(y[3]) << 16);
+          }
+          *reinterpret_cast<uint2*>(page + (h * 2 + (key ? 0 : 1)) * (kHalfBytes / 2)) = out;
+        }
+      }
+      __syncwarp();  // this warp has read the stage
+      if (lane == 0) mbar_arrive(smem_addr(&empty[st]));
+    }
+  }
+  if (failed && lane == 0) atomicOr(p.err, PKV_ERR_TIMEOUT);
 }
 
 }  // namespace
@@ -167,13 +246,12 @@ extern "C" int paged_rope_append(pkv_pool_t* pool, const void* q, long long q_st
   const long long q_row = static_cast<long long>(num_q_heads) * kHeadDim;
   const long long kv_row = static_cast<long long>(pool->num_kv_heads) * kHeadDim;
   if (num_q_heads > kMaxKvHeads * PKV_MAX_GROUP || q_stride < q_row || k_stride < kv_row || v_stride < kv_row ||
-      q_stride % 4 || k_stride % 4 || v_stride % 4)
+      q_stride % 8 || k_stride % 8 || v_stride % 8)
     return -EINVAL;
   if (tokens == 0) return 0;
   if (!q || !k || !v || !q_rot || !slot_map || !positions || !rope_table) return -EINVAL;
-  auto aligned = [](const void* x, uintptr_t n) { return reinterpret_cast<uintptr_t>(x) % n == 0; };
-  if (!aligned(q, 8) || !aligned(k, 8) || !aligned(v, 8) || !aligned(q_rot, 16) || !aligned(rope_table, 16))
-    return -EINVAL;
+  for (const void* x : {q, k, v, static_cast<const void*>(q_rot), rope_table})
+    if (reinterpret_cast<uintptr_t>(x) & 15u) return -EINVAL;
   RopeAppendParams p;
   p.pool = static_cast<uint16_t*>(pool->storage);
   p.num_pages = pool->num_pages;
@@ -193,8 +271,19 @@ extern "C" int paged_rope_append(pkv_pool_t* pool, const void* q, long long q_st
   p.rope_positions = rope_positions;
   p.rot_dim = rot_dim;
   p.err = pool->d_err;
+  // Units of a token: as few as hold its rows, of even size.
+  const int rows = num_q_heads + 2 * pool->num_kv_heads;
+  p.tokens = tokens;
+  p.units = (rows + kUnitRows - 1) / kUnitRows;
+  p.unit_rows = (rows + p.units - 1) / p.units;
+  p.units = (rows + p.unit_rows - 1) / p.unit_rows;
+  const int sms = device_sm_count(pool->device);
+  if (sms < 1) return -EIO;
+  const long long all = static_cast<long long>(tokens) * p.units;
+  const long long most = static_cast<long long>(kRopeCtas) * sms;
+  const unsigned grid = static_cast<unsigned>(all < most ? all : most);
   auto kernel = interleaved ? rope_append_kernel<true> : rope_append_kernel<false>;
-  kernel<<<tokens, kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  kernel<<<grid, kRopeThreads, kRopeStages * kStageBytes, static_cast<cudaStream_t>(stream)>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     record_cuda_error(e);
