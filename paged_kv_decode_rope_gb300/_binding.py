@@ -457,13 +457,41 @@ def paged_kv_split_combine(o_part: torch.Tensor, lse_part: torch.Tensor, num_spl
     _check("paged_kv_split_combine", rc)
 
 
+# A small step's calls last no longer on the GPU than their checks take here
+# (about 0.4 us a tensor), so these check a tensor once, in the order that ends
+# soonest, and leave the wording of a refusal to _shape and _dev.
+
+
 def _arg(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str) -> int:
-    """The pointer of a contiguous CUDA tensor of exactly this type and shape
-    (the checks of _shape and _dev, at the price of one when they hold)."""
-    if type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
+    """The pointer of a contiguous CUDA tensor of exactly this type and shape."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a tensor
+        pass
     _shape(t, shape, name)
     return _dev(t, dtype, name)
+
+
+def _sizes(t: torch.Tensor, ndim: int, name: str) -> tuple:
+    """The shape of a tensor of ndim dimensions."""
+    try:
+        shape = t.shape
+        if len(shape) == ndim:
+            return shape
+    except AttributeError:
+        pass
+    return _shape(t, (None,) * ndim, name)
+
+
+def _bytes(t: torch.Tensor, name: str) -> int:
+    """The pointer of a contiguous uint8 CUDA tensor (a workspace, a table)."""
+    try:
+        if t.dtype is torch.uint8 and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _dev(t, torch.uint8, name)
 
 
 def _optional(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, name: str) -> int | None:
@@ -471,7 +499,7 @@ def _optional(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, name: st
 
 
 def _raw_stream(stream, t: torch.Tensor) -> int:
-    return torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else _stream(stream)
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else _stream(stream)
 
 
 def _typed(t: torch.Tensor, name: str) -> int:
@@ -493,16 +521,16 @@ def paged_tables_build(pool: KVPool, start_pos: torch.Tensor, new_tokens: torch.
     free_head itself), cu_tokens [B+1], seq_lens [B], positions [T],
     slot_map [L,T] int32 out, T the capacity in tokens."""
     i32 = torch.int32
-    layers, batch, max_blocks = _shape(block_tables, (None, None, None), "block_tables")
-    (capacity,) = _shape(positions, (None,), "positions")
-    (num_free,) = _shape(free_pages, (None,), "free_pages")
-    rc = lib().paged_tables_build(
+    tables = layers, batch, max_blocks = _sizes(block_tables, 3, "block_tables")
+    (capacity,) = tokens = _sizes(positions, 1, "positions")
+    (num_free,) = free = _sizes(free_pages, 1, "free_pages")
+    rc = (_lib or lib()).paged_tables_build(
         pool.handle, _arg(start_pos, i32, (batch,), "start_pos"), _arg(new_tokens, i32, (batch,), "new_tokens"),
-        batch, layers, _arg(free_pages, i32, (num_free,), "free_pages"), num_free,
+        batch, layers, _arg(free_pages, i32, free, "free_pages"), num_free,
         _arg(free_head, i32, (1,), "free_head"), _arg(free_head_out, i32, (1,), "free_head_out"),
-        _arg(block_tables, i32, (layers, batch, max_blocks), "block_tables"), max_blocks,
+        _arg(block_tables, i32, tables, "block_tables"), max_blocks,
         _arg(cu_tokens, i32, (batch + 1,), "cu_tokens"), _arg(seq_lens, i32, (batch,), "seq_lens"),
-        _arg(positions, i32, (capacity,), "positions"), _arg(slot_map, i32, (layers, capacity), "slot_map"),
+        _arg(positions, i32, tokens, "positions"), _arg(slot_map, i32, (layers, capacity), "slot_map"),
         capacity, _raw_stream(stream, block_tables))
     if rc:
         raise PkvError("paged_tables_build", rc)
@@ -525,7 +553,7 @@ def paged_rope_table_build_freqs(inv_freq, num_positions: int, table: torch.Tens
 def _token_rows(t: torch.Tensor, tokens: int, heads: int, name: str) -> tuple[int, int]:
     """Pointer and token stride (elements) of bf16 [tokens][heads][64] whose
     heads are contiguous: the whole tensor, or a slice of a projection."""
-    if type(t) is not torch.Tensor or t.shape != (tokens, heads, HEAD_DIM):
+    if _sizes(t, 3, name) != (tokens, heads, HEAD_DIM):
         _shape(t, (tokens, heads, HEAD_DIM), name)
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -545,15 +573,15 @@ def paged_rope_append(pool: KVPool, q: torch.Tensor, k: torch.Tensor, v: torch.T
     [T] int32 (one layer's slots; negative: not stored). q_rot [T,Hq,64] fp32
     out; positions [T] int32, rows of rope_table. q, k and v may be slices of
     one projection's output (any token stride)."""
-    tokens, hq, _ = _shape(q, (None, None, HEAD_DIM), "q")
+    tokens, hq, _ = _sizes(q, 3, "q")
     hkv = pool.num_kv_heads
     qp, qs = _token_rows(q, tokens, hq, "q")
     kp, ks = _token_rows(k, tokens, hkv, "k")
     vp, vs = _token_rows(v, tokens, hkv, "v")
-    rc = lib().paged_rope_append(
+    rc = (_lib or lib()).paged_rope_append(
         pool.handle, qp, qs, kp, ks, vp, vs, _arg(q_rot, torch.float32, (tokens, hq, HEAD_DIM), "q_rot"),
         _arg(slot_map, torch.int32, (tokens,), "slot_map"), _arg(positions, torch.int32, (tokens,), "positions"),
-        tokens, hq, _dev(rope_table, torch.uint8, "rope_table", 1), rope_table_rows(rope_table), int(rot_dim),
+        tokens, hq, _bytes(rope_table, "rope_table"), rope_table.numel() // ROPE_TABLE_BYTES_PER_ROW, int(rot_dim),
         1 if interleaved else 0, _raw_stream(stream, q))
     if rc:
         raise PkvError("paged_rope_append", rc)
@@ -572,15 +600,15 @@ def paged_gqa_decode_scored(pool: KVPool, q_rot: torch.Tensor, out: torch.Tensor
     (alibi_slopes [Hq] fp32) and windowed (window > 0) scores, over keys from
     first_keys [B] int32 on. q_rot [B,Hq,64] fp32, out [B,Hq,64] fp32 or
     bf16; workspace from alloc_decode_workspace()."""
-    batch, hq, _ = _shape(q_rot, (None, None, HEAD_DIM), "q_rot")
-    _, max_blocks = _shape(block_tables, (batch, None), "block_tables")
+    batch, hq, _ = _sizes(q_rot, 3, "q_rot")
+    _, max_blocks = _sizes(block_tables, 2, "block_tables")
+    rows = (batch, hq, HEAD_DIM)
     out_type = _typed(out, "out")
-    rc = lib().paged_gqa_decode_scored(
-        pool.handle, _arg(q_rot, torch.float32, (batch, hq, HEAD_DIM), "q_rot"),
-        _arg(out, out.dtype, (batch, hq, HEAD_DIM), "out"), out_type,
+    rc = (_lib or lib()).paged_gqa_decode_scored(
+        pool.handle, _arg(q_rot, torch.float32, rows, "q_rot"), _arg(out, out.dtype, rows, "out"), out_type,
         _arg(block_tables, torch.int32, (batch, max_blocks), "block_tables"), max_blocks,
         _arg(seq_lens, torch.int32, (batch,), "seq_lens"), _optional(first_keys, torch.int32, (batch,), "first_keys"),
-        batch, hq, _scoring(scale, softcap, alibi_slopes, window, hq), _dev(workspace, torch.uint8, "workspace", 1),
+        batch, hq, _scoring(scale, softcap, alibi_slopes, window, hq), _bytes(workspace, "workspace"),
         workspace.numel(), _raw_stream(stream, q_rot))
     if rc:
         raise PkvError("paged_gqa_decode_scored", rc)
@@ -599,18 +627,18 @@ def paged_gqa_prefill_scored(pool: KVPool, q_rot: torch.Tensor, out: torch.Tenso
     q_rot [T,Hq,64] fp32, out [T,Hq,64] fp32 or bf16, block_tables
     [B,max_blocks], cu_tokens [B+1], start_pos [B] int32; workspace from
     alloc_prefill_workspace()."""
-    total, hq, _ = _shape(q_rot, (None, None, HEAD_DIM), "q_rot")
-    batch, max_blocks = _shape(block_tables, (None, None), "block_tables")
+    total, hq, _ = _sizes(q_rot, 3, "q_rot")
+    tables = batch, max_blocks = _sizes(block_tables, 2, "block_tables")
+    rows = (total, hq, HEAD_DIM)
     i32 = torch.int32
     out_type = _typed(out, "out")
-    rc = lib().paged_gqa_prefill_scored(
-        pool.handle, _arg(q_rot, torch.float32, (total, hq, HEAD_DIM), "q_rot"),
-        _arg(out, out.dtype, (total, hq, HEAD_DIM), "out"), out_type,
-        _arg(block_tables, i32, (batch, max_blocks), "block_tables"), max_blocks,
+    rc = (_lib or lib()).paged_gqa_prefill_scored(
+        pool.handle, _arg(q_rot, torch.float32, rows, "q_rot"), _arg(out, out.dtype, rows, "out"), out_type,
+        _arg(block_tables, i32, tables, "block_tables"), max_blocks,
         _arg(cu_tokens, i32, (batch + 1,), "cu_tokens"), _arg(start_pos, i32, (batch,), "start_pos"),
         _optional(prefix_lens, i32, (batch,), "prefix_lens"), _optional(doc_starts, i32, (total,), "doc_starts"),
         batch, total, hq, _scoring(scale, softcap, alibi_slopes, window, hq),
-        _dev(workspace, torch.uint8, "workspace", 1), workspace.numel(), _raw_stream(stream, q_rot))
+        _bytes(workspace, "workspace"), workspace.numel(), _raw_stream(stream, q_rot))
     if rc:
         raise PkvError("paged_gqa_prefill_scored", rc)
 
@@ -637,19 +665,19 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None, logprobs:
     entropy [R] fp32 of each row; its K most likely tokens top_ids [R,K] int32
     with top_logprobs [R,K] fp32 (K up to 32, the lower id first among
     equals). Outputs that are None are left out."""
-    rows, vocab = _shape(logits, (None, None), "logits")
+    rows, vocab = _sizes(logits, 2, "logits")
     if not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor")
     stride, step = logits.stride()
     if step != 1 and vocab > 1:
         raise ValueError("logits must have contiguous rows")
-    top = 0 if top_ids is None else _shape(top_ids, (rows, None), "top_ids")[1]
+    top = 0 if top_ids is None else _sizes(top_ids, 2, "top_ids")[1]
     f32, i32 = torch.float32, torch.int32
-    rc = lib().token_logprobs(
+    rc = (_lib or lib()).token_logprobs(
         logits.data_ptr(), _typed(logits, "logits"), stride if rows > 1 else vocab, rows, vocab, scale,
         _optional(targets, i32, (rows,), "targets"), top, _optional(logprobs, f32, (rows,), "logprobs"),
         _optional(entropy, f32, (rows,), "entropy"), _optional(top_ids, i32, (rows, top), "top_ids"),
-        _optional(top_logprobs, f32, (rows, top), "top_logprobs"), _dev(workspace, torch.uint8, "workspace", 1),
+        _optional(top_logprobs, f32, (rows, top), "top_logprobs"), _bytes(workspace, "workspace"),
         workspace.numel(), _raw_stream(stream, logits))
     if rc:
         raise PkvError("token_logprobs", rc)

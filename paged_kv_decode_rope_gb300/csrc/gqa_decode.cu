@@ -1194,7 +1194,7 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
           // segments long enough to span three or more CTAs, and their kernel
           // has the registers to spare; in the register-capped kernel of 1-4
           // heads the extra code cost 0.2 us per layer where it never ran.
-          if constexpr (G > 4) {
+          if constexpr (G > 4 || kScored) {
             if (g_last - g_first >= 2 && !failed) {
               done = gather_groups_staged<G>(all, pc, p.slots, ring0, grp, g_first, g_last, g8,
                                              tig, lane);

@@ -11,7 +11,8 @@
 // shared-memory stages and runs ahead into the next row while the others pick
 // the alternatives of this one, so that the memory never idles (a CTA a row,
 // loading as it went: 128 us for 2048 rows of 128256 bf16, 60% of the copy
-// bandwidth). What bounds it
+// bandwidth). Rows are handed out from a counter: with a fixed share for every
+// CTA the slowest SM's memory path set the time (33% over the median's). What bounds it
 // is that stream; the arithmetic (unpack, difference, product, exp2, two sums an
 // element) is the next limit, about half of it.
 //
@@ -19,18 +20,29 @@
 // are a group; a group's best logit is known after the stream. The K groups
 // with the best ones (ties: the group whose best comes first) hold the row's K
 // best logits, since the K group bests are K logits that no logit outside
-// these groups beats. So only K groups of the CTA's threads are read again
-// (from L2: K / kLogThreads of the row), and of them only the logits not below
-// the K-th group best are kept, about K of them. Keys are 64-bit: the logit as
-// an ordered integer above, the complement of its index below, so that equal
-// logits rank by index and all keys differ; any number of ties (a row of equal
-// logits, or masked to -inf) costs no more than others.
+// these groups beats. Of these groups only the logits not below the K-th group
+// best are wanted, about K in all; unless a group's second best vector reaches
+// that bound too, they are all in the vector of its best, which its thread
+// keeps; in the few other cases the group is read again. Keys are 64-bit:
+// the logit as an ordered integer above, the complement of its index below, so
+// that equal logits rank by index and all keys differ; any number of ties (a
+// row of equal logits, or masked to -inf) is resolved by the same steps.
 //
-// Few rows are split over several CTAs each, as many as give every SM work;
-// the last CTA of a row to finish (a ticket in the workspace) merges the
-// pieces in their order, so the result does not depend on which one it is.
+// This selection is a chain of short steps, and its latency is what the copies
+// running ahead into the CTA's next row must cover. First done by sorting the
+// group bests and the candidates in bitonic networks and reading the K groups
+// again, it took 25,000 cycles a row next to the stream's 42,000. So the K-th
+// group best is found in two steps (a bound from the ceil(K / warps)-th best of
+// each warp, by warp-wide maxima, leaves about twice K groups; those, and later
+// the candidates, are ranked by counting).
+//
+// Few rows, and the rows left over when the CTAs have taken whole rounds, are
+// split over several CTAs each; the last CTA of a row to finish (a ticket in the
+// workspace) merges the pieces in their order, so the result does not depend
+// on which one it is.
 #include <atomic>
 #include <cerrno>
+#include <climits>
 #include <cmath>
 
 #include "f32x2.cuh"
@@ -41,29 +53,28 @@ namespace pkv {
 namespace {
 
 constexpr int kLogThreads = 256;
-constexpr int kLogCtas = 4;         // CTAs a SM
+constexpr int kLogCtas = 3;         // CTAs a SM
 constexpr int kLogWarps = kLogThreads / 32;
 constexpr int kTop = PKV_MAX_TOP;
 constexpr int kUnroll = 4;          // vectors a thread takes from a stage
-constexpr int kLogStages = 3;
+constexpr int kLogStages = 4;
 constexpr int kStageVectors = kUnroll * kLogThreads;
 constexpr int kLogBlock = kLogThreads + 32;  // and the copying warp
-constexpr int kCandidates = 256;    // keys the second look keeps at once
+constexpr int kCandidates = 256;    // keys ranked at once
 constexpr int kMaxSplits = 64;
-#ifndef KMIN
-#define KMIN 4
-#endif
-constexpr int kMinSplitVectors = KMIN * kLogThreads;  // smallest piece of a split row
+constexpr int kMinSplitVectors = 4 * kLogThreads;  // smallest piece of a split row
 constexpr float kLogSlack = 8.f;
 // In the stream a logit below kLowest counts as kLowest, so that -inf makes
 // e^y = 0 and 0 * y = 0, not NaN; only a logit above kFloor sets the reference
 // (100 times smaller, so that e^y of kLowest is 0 for any scale in kMinScale
 // .. 1 / kMinScale). A CTA whose logits are all at or below kFloor (masked by
-// the type's lowest value) takes its sums again without these limits.
-constexpr float kLowest = -1e30f, kFloor = -1e28f;
+// the type's lowest value), or whose reference is above kHuge (so that a
+// difference could overflow when scaled), takes its sums again without these
+// limits.
+constexpr float kLowest = -1e30f, kFloor = -1e28f, kHuge = 1e32f;
 constexpr float kMinScale = 1e-6f;
 static_assert(kTop == 32, "a sorted list is one key a lane");
-static_assert(kCandidates == kLogThreads, "a warp sorts 32 candidates");
+static_assert(kCandidates == kLogThreads, "every group can be a candidate");
 
 struct LogprobsParams {
   const uint8_t* logits;
@@ -77,11 +88,14 @@ struct LogprobsParams {
   float* entropy;
   int32_t* top_ids;
   float* top_logprobs;
-  int splits;          // CTAs a row
-  int split_vectors;   // vectors of each
-  int* tickets;        // [rows], zero between calls
-  float4* sums;        // [rows][splits] {M, S, Z, -} (base 2)
-  uint64_t* keys;      // [rows][splits][kTop]
+  int whole;           // rows 0 .. whole - 1 are a piece each
+  int splits;          // pieces of each row after them
+  int split_vectors;   // vectors of such a piece
+  int pieces;          // of all rows
+  int* counter;        // pieces handed out past the first round, zero between calls
+  int* tickets;        // [split rows], zero between calls
+  float4* sums;        // [split pieces] {m, S, Z, -}
+  uint64_t* keys;      // [split pieces][kTop]
 };
 
 // A logit as an integer of the same order (-0 as +0, NaN as -inf), and back.
@@ -105,14 +119,6 @@ __device__ __forceinline__ int index_of(uint64_t key) {
 __device__ __forceinline__ uint64_t exchange(uint64_t key, int j, bool larger) {
   const uint64_t o = __shfl_xor_sync(kFull, key, j);
   return (key > o) == larger ? key : o;
-}
-// The warp's 32 keys, largest first.
-__device__ __forceinline__ uint64_t sort32(uint64_t key, int lane) {
-#pragma unroll
-  for (int k = 2; k <= 32; k <<= 1)
-#pragma unroll
-    for (int j = k >> 1; j; j >>= 1) key = exchange(key, j, ((lane & j) == 0) == ((lane & k) == 0));
-  return key;
 }
 // The 32 largest of two lists sorted largest first, sorted again.
 __device__ __forceinline__ uint64_t merge32(uint64_t a, uint64_t b, int lane) {
@@ -216,19 +222,21 @@ struct Piece {
   static constexpr int kE = Vec<T>::kElems;
   const uint8_t* base;   // element 0
   const uint8_t* vbase;  // vector 0
-  int row, off, vocab;
+  int row, split_row, off, vocab;  // split_row: among the split rows, -1 for a whole one
   int v0, v1;            // the piece's vectors
   int whole0, whole1;    // vectors that lie inside the row
   __device__ Piece(const LogprobsParams& p, int piece) {
-    row = piece / p.splits;
-    const int split = piece - row * p.splits;
+    const int rest = piece - p.whole;
+    split_row = rest < 0 ? -1 : rest / p.splits;
+    const int split = rest < 0 ? 0 : rest - split_row * p.splits;
+    row = rest < 0 ? piece : p.whole + split_row;
     base = p.logits + static_cast<size_t>(row) * p.row_bytes;
     off = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15u) / sizeof(T));
     vbase = base - off * sizeof(T);
     vocab = p.vocab;
     const int nv = static_cast<int>((static_cast<long long>(off) + vocab + kE - 1) / kE);
-    v0 = split * p.split_vectors;
-    v1 = min(nv, v0 + p.split_vectors);
+    v0 = rest < 0 ? 0 : min(nv, split * p.split_vectors);
+    v1 = rest < 0 ? nv : min(nv, v0 + p.split_vectors);
     whole0 = off ? 1 : 0;
     whole1 = (off + vocab) % kE ? nv - 1 : nv;
   }
@@ -260,20 +268,30 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
   using V = Vec<T>;
   constexpr int kE = V::kElems;
   extern __shared__ __align__(128) uint8_t s_ring[];
-  __shared__ __align__(8) uint64_t full[kLogStages], empty[kLogStages];
-  __shared__ uint64_t s_list[kLogWarps][32];
-  __shared__ uint64_t s_cand[kCandidates];
-  __shared__ Sums s_sums[kLogWarps];
-  __shared__ int s_group[kTop];
+  __shared__ __align__(8) uint64_t full[kLogStages], empty[kLogStages], piece_full[2], piece_empty[2];
+  __shared__ int s_piece[2];  // the pieces to work on, in turns; -1: no more
+  __shared__ uint64_t s_list[kLogWarps][32];  // merging pieces
+  __shared__ __align__(16) uint64_t s_cand[kCandidates];
+  __shared__ uint64_t s_best[kTop];           // the piece's best, in order
+  __shared__ float s_ref[kLogWarps];
+  __shared__ uint32_t s_least[kLogWarps];
+  __shared__ float2 s_sums[kLogWarps];
+  __shared__ int s_group[kTop];  // groups to read again: thread, best vector
+  __shared__ int s_group_best[kTop], s_group_end[kTop];
+  __shared__ int s_groups;
   __shared__ uint64_t s_bound;
   __shared__ int s_count, s_last;
   __shared__ uint32_t s_top;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int pieces = p.rows * p.splits;
+  const int pieces = p.pieces;
   if (tid == 0) {
     for (int s = 0; s < kLogStages; ++s) {
       mbar_init(smem_addr(&full[s]), 1);
       mbar_init(smem_addr(&empty[s]), kLogWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&piece_full[i]), 1);
+      mbar_init(smem_addr(&piece_empty[i]), kLogWarps);
     }
   }
   fence_mbar_init();
@@ -284,7 +302,21 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
     // ---- the copies: every piece's whole vectors, kStageVectors a stage ----
     if (lane != 0) return;
     bool failed = false;
-    for (int piece = blockIdx.x; piece < pieces && !failed; piece += gridDim.x) {
+    for (int n = 0; !failed; ++n) {
+      int piece = blockIdx.x;
+      if (n > 0) {
+        const int v = atomicAdd(p.counter, 1);
+        piece = static_cast<int>(gridDim.x) + v;
+        if (v == pieces - 1) *p.counter = 0;  // every CTA has had its last answer: ready for the next call
+      }
+      if (piece >= pieces) piece = -1;
+      if (n >= 2 && !mbar_wait_bounded(smem_addr(&piece_empty[n & 1]), ((n >> 1) - 1) & 1)) {
+        failed = true;
+        break;
+      }
+      s_piece[n & 1] = piece;
+      mbar_arrive(smem_addr(&piece_full[n & 1]));
+      if (piece < 0) break;
       const Piece<T> r(p, piece);
       for (int c = r.v0; c < r.v1; c += kStageVectors, ++chunk) {
         const int st = chunk % kLogStages, use = chunk / kLogStages;
@@ -310,7 +342,12 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
     return;
   }
 
-  for (int piece = blockIdx.x; piece < pieces; piece += gridDim.x) {
+  for (int n = 0;; ++n) {
+    if (!mbar_wait_bounded(smem_addr(&piece_full[n & 1]), (n >> 1) & 1)) break;  // (only after the copies gave up)
+    const int piece = s_piece[n & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&piece_empty[n & 1]));
+    if (piece < 0) break;
     const Piece<T> r(p, piece);
     const int row = r.row, v0 = r.v0, v1 = r.v1;
     // ---- the stream ----
@@ -319,15 +356,22 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
     // limit = ref + kLogSlack / c2.
     float ref = -INFINITY, limit = kFloor;
     const float slack = kLogSlack / p.c2;
-    float best = -INFINITY;
+    float best = -INFINITY, next = -INFINITY;  // the largest logit, and of the vectors without it
     int best_v = v0 + tid;
-    uint64_t s2 = f32x2(0.f, 0.f), z2 = s2;
+    uint4 best_w = make_uint4(0u, 0u, 0u, 0u);
+    // the target's logit, wanted at the end
+    const int target = p.targets && tid == 0 ? p.targets[row] : -1;
+    const float target_x =
+        target >= 0 && target < p.vocab ? V::value(V::raw(r.base + static_cast<size_t>(target) * sizeof(T))) : NAN;
+    uint64_t s2 = f32x2(0.f, 0.f), z2 = s2, nr = s2;  // nr: -ref, 0 while there is none
     const uint64_t cc = f32x2(p.c2, p.c2);
     auto take = [&](const uint4& w, int v) {
       const float m = V::max(w);
+      next = fmaxf(next, fminf(m, best));
       if (m > best) {
         best = m;
         best_v = v;
+        best_w = w;
       }
       if (m > limit) {  // move the reference: the first logit, or one far above it
         if (ref != -INFINITY) {
@@ -338,9 +382,8 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
         }
         ref = m;
         limit = m + slack;
+        nr = f32x2(-m, -m);
       }
-      const float nref = ref == -INFINITY ? 0.f : -ref;
-      const uint64_t nr = f32x2(nref, nref);
 #pragma unroll
       for (int i = 0; i < kE / 2; ++i) {
         const float2 x = V::pair(w, i);
@@ -371,126 +414,206 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
       if (lane == 0) mbar_arrive(smem_addr(&empty[st]));
     }
 
-    // ---- the sums of the CTA ----
+    // ---- the sums and the K best of the CTA's piece ----
+    // One exchange for both: the warps' largest references, and their
+    // ceil(K / warps)-th best groups, the least of which bounds the K-th best
+    // group of all from below.
+    const uint32_t mine = v0 + tid < v1 ? ordered(best) : 0u;  // 0: no group
+    {
+      const float wref = unordered(__reduce_max_sync(kFull, ordered(ref)));
+      uint32_t left = mine, nth = 0u;
+      for (int k = 0; k < p.top; k += kLogWarps) {
+        nth = __reduce_max_sync(kFull, left);
+        const unsigned who = __ballot_sync(kFull, left == nth);
+        if (lane == __ffs(who) - 1) left = 0u;
+      }
+      if (lane == 0) {
+        s_ref[warp] = wref;
+        s_least[warp] = nth;
+      }
+      if (tid == 0) {
+        s_top = 0u;
+        s_count = 0;
+      }
+    }
+    compute_sync();
     Sums all;
+    all.m = s_ref[0];
+    uint32_t least = s_least[0];
+#pragma unroll
+    for (int w = 1; w < kLogWarps; ++w) {
+      all.m = fmaxf(all.m, s_ref[w]);
+      least = min(least, s_least[w]);
+    }
     {
       const float2 s = unpack_f32x2(s2), z = unpack_f32x2(z2);
-      all = Sums{ref, late ? NAN : s.x + s.y, z.x + z.y};
-    }
-    auto share_sums = [&]() {  // of each warp
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        Sums t;
-        t.m = __shfl_xor_sync(kFull, all.m, o);
-        t.s = __shfl_xor_sync(kFull, all.s, o);
-        t.z = __shfl_xor_sync(kFull, all.z, o);
-        all.join(t, p.c2);
-      }
-      if (lane == 0) s_sums[warp] = all;
-      compute_sync();
-    };
-    if (tid == 0) s_top = 0u;
-    share_sums();
-    bool any = false;
-#pragma unroll
-    for (int w = 0; w < kLogWarps; ++w) any |= s_sums[w].m != -INFINITY;
-    if (!any) {  // nothing above kFloor: rare
-      atomicMax(&s_top, ordered(best));
-      compute_sync();
-      const float top = unordered(s_top);
-      if (top != -INFINITY) {
-        all = Sums{top, 0.f, 0.f};
-        for (int u = v0 + tid; u < v1; u += kLogThreads) {
-          const uint4 w = r.load(u);
-#pragma unroll
-          for (int e = 0; e < kE; ++e) {
-            const float y = (V::get(w, e) - top) * p.c2, f = exp2f(y);
-            all.s += f;
-            if (f > 0.f) all.z += f * y;
-          }
-        }
-        share_sums();
-      }
-    }
-
-    // ---- the K best of the CTA's piece ----
-    uint64_t key = 0;
-    if (p.top > 0) {
-      // each group by its best logit and the vector that holds it
-      key = v0 + tid < v1 ? key_of(best, best_v) : 0;
-      key = merge_warps(sort32(key, lane), s_list, kLogWarps);
-      if (warp == 0) {
-        s_group[lane] = key && lane < p.top ? (index_of(key) - v0) % kLogThreads : -1;
-        if (lane == p.top - 1) {
-          // no logit below the K-th group's best is needed (index: the last one
-          // its vector can hold)
-          s_bound = key ? (key >> 32 << 32 | (0xffffffffu - static_cast<uint32_t>(index_of(key) * kE - r.off + kE - 1)))
-                        : 1;
-        }
-        if (lane == 0) s_count = 0;
-      }
-      compute_sync();
-      for (;;) {
-        const uint64_t bound = s_bound;
-        const float least = unordered(static_cast<uint32_t>(bound >> 32));
-        for (int g = warp; g < p.top; g += kLogWarps) {
-          if (s_group[g] < 0) continue;
-          for (int u = v0 + s_group[g] + lane * kLogThreads; u < v1; u += 32 * kLogThreads) {
+      all.s = late ? NAN : s.x + s.y;
+      all.z = z.x + z.y;
+      if (all.m == -INFINITY || all.m > kHuge) {  // rare
+        atomicMax(&s_top, mine);
+        compute_sync();
+        const float top = unordered(s_top);
+        if (s_top != 0u && top != -INFINITY) {
+          all = Sums{top, 0.f, 0.f};
+          for (int u = v0 + tid; u < v1; u += kLogThreads) {
             const uint4 w = r.load(u);
-            if (bound > 1 && V::max(w) < least) continue;
 #pragma unroll
             for (int e = 0; e < kE; ++e) {
-              const int i = u * kE - r.off + e;
-              const uint64_t k = key_of(V::get(w, e), i);
-              if (i >= 0 && i < p.vocab && k >= bound) {
-                const int at = atomicAdd(&s_count, 1);
-                if (at < kCandidates) s_cand[at] = k;
+              const float y = (V::get(w, e) - top) * p.c2, f = exp2f(y);
+              all.s += f;
+              if (f > 0.f) all.z += f * y;
+            }
+          }
+        }
+      } else if (ref != -INFINITY) {  // to the CTA's reference; a thread without one has 0 (or NaN)
+        const float d = (ref - all.m) * p.c2, f = fast_exp2(d);
+        all.z = f > 0.f ? f * (all.z + all.s * d) : f * all.s;
+        all.s *= f;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        all.s += __shfl_xor_sync(kFull, all.s, o);
+        all.z += __shfl_xor_sync(kFull, all.z, o);
+      }
+      if (lane == 0) s_sums[warp] = make_float2(all.s, all.z);
+    }
+    // the number of the n keys of s_cand above this one
+    auto rank = [&](uint64_t key, int n) {
+      int above = 0;
+      for (int i = 0; i < n; i += 4) {  // (zeros fill up a last four)
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(s_cand + i);
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(s_cand + i + 2);
+        above += (a.x > key) + (a.y > key) + (b.x > key) + (b.y > key);
+      }
+      return above;
+    };
+    if (p.top > 0) {
+      // the groups not below the bound, each by its best logit and the vector
+      // that holds it; of these the K best
+      const uint64_t key = mine ? static_cast<uint64_t>(mine) << 32 | (0xffffffffu - static_cast<uint32_t>(best_v)) : 0;
+      // (of a warp's groups of nothing but -inf only the first K can count: they
+      // rank by thread)
+      bool in = mine && mine >= least;
+      const unsigned nothing = __ballot_sync(kFull, in && best == -INFINITY);
+      if (best == -INFINITY && __popc(nothing & ((1u << lane) - 1)) >= p.top) in = false;
+      const unsigned who = __ballot_sync(kFull, in);
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&s_count, __popc(who));
+      at = __shfl_sync(kFull, at, 0) + __popc(who & ((1u << lane) - 1));
+      if (in) s_cand[at] = key;
+      if (tid < p.top) s_best[tid] = 0;  // (a piece may hold fewer than K)
+      if (tid == 0) s_bound = 1;
+      compute_sync();
+      const int groups = s_count;
+      if (tid >= groups && tid < ((groups + 3) & ~3)) s_cand[tid] = 0;
+      compute_sync();
+      int place = p.top;  // of this thread's group among the K best
+      if (in) {
+        if (best == -INFINITY) best_w = r.load(best_v);  // (all -inf or NaN: its first vector)
+        place = rank(key, groups);
+        // no logit below the K-th group's best is needed (index: the last one
+        // its vector can hold)
+        if (place == p.top - 1)
+          s_bound = key >> 32 << 32 | (0xffffffffu - static_cast<uint32_t>(best_v * kE - r.off + kE - 1));
+      }
+      for (;;) {
+        if (tid == 0) s_count = s_groups = 0;
+        compute_sync();
+        const uint64_t bound = s_bound;
+        const float low = bound > 1 ? unordered(static_cast<uint32_t>(bound >> 32)) : -INFINITY;
+        const int last_v = bound > 1 ? (index_of(bound) + r.off) / kE : INT_MAX;  // logits equal to low count up to here
+        // the logit at place e of vector v, if it is one and not below the bound
+        auto look = [&](float x, int v, int e) {
+          const int index = v * kE - r.off + e;
+          const uint64_t k = index >= 0 && index < p.vocab ? key_of(x, index) : 0;
+          if (k < bound) return;
+          const int slot = atomicAdd(&s_count, 1);
+          if (slot < kCandidates) s_cand[slot] = k;
+        };
+        if (place < p.top) {
+#pragma unroll
+          for (int e = 0; e < kE; ++e)
+            if (!(V::get(best_w, e) < low)) look(V::get(best_w, e), best_v, e);
+          if (!(next < low)) {  // the group may hold more
+            const int slot = atomicAdd(&s_groups, 1);
+            s_group[slot] = tid;
+            s_group_best[slot] = best_v;
+            s_group_end[slot] = next > low || last_v >= v1 ? v1 : last_v + 1;  // nothing past it counts
+          }
+        }
+        compute_sync();
+        for (int g = warp; g < s_groups; g += kLogWarps) {
+          constexpr int kAhead = 2;  // vectors a lane loads at once
+          for (int u0 = v0; u0 < s_group_end[g]; u0 += kAhead * 32 * kLogThreads) {
+            uint4 w[kAhead];
+            bool maybe[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+              const int u = u0 + s_group[g] + (lane + 32 * i) * kLogThreads;
+              maybe[i] = u < s_group_end[g] && u != s_group_best[g];
+              w[i] = make_uint4(0u, 0u, 0u, 0u);
+              if (maybe[i]) w[i] = r.load(u);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+              // a vector with a logit not below the bound is taken apart, a logit a
+              // lane (one of NaN has no largest: taken apart as well)
+              const int u = u0 + s_group[g] + (lane + 32 * i) * kLogThreads;
+              const float m = V::max(w[i]);
+              for (unsigned hit = __ballot_sync(kFull, maybe[i] && (u <= last_v ? !(m < low) : m > low)); hit;
+                   hit &= hit - 1) {
+                const int src = __ffs(hit) - 1;
+                const uint4 x = make_uint4(__shfl_sync(kFull, w[i].x, src), __shfl_sync(kFull, w[i].y, src),
+                                           __shfl_sync(kFull, w[i].z, src), __shfl_sync(kFull, w[i].w, src));
+                if (lane < kE) look(V::get(x, lane % kE), u0 + s_group[g] + (src + 32 * i) * kLogThreads, lane);
               }
             }
           }
         }
         compute_sync();
-        const int n = s_count;
-        const int lists = min((min(n, kCandidates) + 31) / 32, kLogWarps);
-        key = tid < min(n, kCandidates) ? s_cand[tid] : 0;
-        if (warp < lists) key = sort32(key, lane);
-        key = merge_warps(key, s_list, lists);
+        const int n = s_count, kept = min(n, kCandidates);
+        if (tid >= kept && tid < ((kept + 3) & ~3)) s_cand[tid] = 0;
+        compute_sync();
+        if (tid < kept) {
+          const uint64_t k = s_cand[tid];
+          const int above = rank(k, kept);
+          if (above < p.top) s_best[above] = k;
+          if (above == p.top - 1) s_bound = k;
+        }
+        compute_sync();
         if (n <= kCandidates) break;
         // More than fit: the K-th of those kept is a higher bound (all keys
         // differ, and more than K were kept), so look again.
-        compute_sync();
-        if (tid == p.top - 1) s_bound = key;
-        if (tid == 0) s_count = 0;
-        compute_sync();
       }
+    } else {
+      compute_sync();
     }
+    uint64_t key = lane < p.top ? s_best[lane] : 0;  // (only warp 0's is used)
 
     // ---- the row's result: from this piece, or from all of them ----
     if (warp == 0) {
-      all = lane < kLogWarps ? s_sums[lane] : Sums{-INFINITY, 0.f, 0.f};
+      all.s = all.z = 0.f;
 #pragma unroll
-      for (int o = kLogWarps / 2; o; o >>= 1) {
-        Sums t;
-        t.m = __shfl_down_sync(kFull, all.m, o);
-        t.s = __shfl_down_sync(kFull, all.s, o);
-        t.z = __shfl_down_sync(kFull, all.z, o);
-        all.join(t, p.c2);
+      for (int w = 0; w < kLogWarps; ++w) {
+        all.s += s_sums[w].x;
+        all.z += s_sums[w].y;
       }
     }
-    bool mine = true;  // this CTA writes the row's result
-    if (p.splits > 1) {
+    bool writes = true;  // this CTA writes the row's result
+    if (r.split_row >= 0) {
+      const int slot = piece - p.whole;
       if (warp == 0) {
-        if (lane < p.top) p.keys[static_cast<size_t>(piece) * kTop + lane] = key;
-        if (lane == 0) p.sums[piece] = make_float4(all.m, all.s, all.z, 0.f);
+        if (lane < p.top) p.keys[static_cast<size_t>(slot) * kTop + lane] = key;
+        if (lane == 0) p.sums[slot] = make_float4(all.m, all.s, all.z, 0.f);
         __threadfence();
         __syncwarp();
-        if (lane == 0) s_last = atomicAdd(&p.tickets[row], 1) == p.splits - 1;
+        if (lane == 0) s_last = atomicAdd(&p.tickets[r.split_row], 1) == p.splits - 1;
       }
       compute_sync();
-      mine = s_last;
-      if (mine) {
+      writes = s_last;
+      if (writes) {
         __threadfence();
-        const size_t first = static_cast<size_t>(row) * p.splits;
+        const size_t first = static_cast<size_t>(r.split_row) * p.splits;
         if (p.top > 0) {
           const int lists = min(p.splits, kLogWarps);
           key = 0;
@@ -515,22 +638,18 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
             t.z = __shfl_down_sync(kFull, all.z, o);
             all.join(t, p.c2);
           }
-          if (lane == 0) p.tickets[row] = 0;
+          if (lane == 0) p.tickets[r.split_row] = 0;
         }
       }
     }
-    if (mine && warp == 0) {
+    if (writes && warp == 0) {
       const float m = __shfl_sync(kFull, all.m, 0), s = __shfl_sync(kFull, all.s, 0), z = __shfl_sync(kFull, all.z, 0);
       // without a finite logit there is no distribution
       const float log_s = m == -INFINITY ? NAN : logf(s);
       constexpr float kLn2f = 0.6931471805599453f;
       auto logp = [&](float x) { return (x - m) * p.scale - log_s; };
       if (lane == 0) {
-        if (p.targets) {
-          const int t = p.targets[row];
-          p.logprobs[row] =
-              t >= 0 && t < p.vocab ? logp(V::value(V::raw(r.base + static_cast<size_t>(t) * sizeof(T)))) : NAN;
-        }
+        if (p.targets) p.logprobs[row] = logp(target_x);
         if (p.entropy) p.entropy[row] = log_s - z / s * kLn2f;
       }
       if (lane < p.top) {
@@ -544,14 +663,21 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// CTAs a row: as many as run at once (rounded down: a few CTAs of a second
-// round would double the time), none smaller than kMinSplitVectors.
-int splits_for(int rows, long long vectors, int sms) {
-  const long long want = static_cast<long long>(kLogCtas) * sms / rows;
+// How the rows are cut for `ctas` CTAs: whole rounds of a row a CTA first; the
+// rows left over (or all, when they are fewer) are split over as many CTAs as
+// run at once, rounded down (a few pieces of a further round would double the
+// time), no piece smaller than kMinSplitVectors. `vectors` as for a row that
+// starts anywhere.
+struct Cut {
+  int whole, splits;
+};
+Cut cut(int rows, long long vectors, int ctas) {
+  const int rest = rows % ctas;
+  if (rest == 0) return {rows, 1};
   long long n = vectors / kMinSplitVectors;
-  if (n > want) n = want;
+  if (n > ctas / rest) n = ctas / rest;
   if (n > kMaxSplits) n = kMaxSplits;
-  return n < 1 ? 1 : static_cast<int>(n);
+  return n < 2 ? Cut{rows, 1} : Cut{rows - rest, static_cast<int>(n)};
 }
 
 }  // namespace
@@ -562,13 +688,13 @@ extern "C" {
 size_t token_logprobs_workspace_bytes(int rows, int vocab, int top) {
   using namespace pkv;
   if (rows < 1 || vocab < 1 || top < 0 || top > PKV_MAX_TOP || top > vocab) return 0;
-  // room for either type: fp32 rows have more vectors, so at least as many pieces
+  // the counter, a ticket a row, and room for as many split pieces as CTAs run at once
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return 0;
   const int sms = device_sm_count(device);
   if (sms < 1) return 0;
-  const size_t pieces = static_cast<size_t>(rows) * splits_for(rows, static_cast<long long>(vocab) / 4 + 2, sms);
-  return align256(sizeof(int) * static_cast<size_t>(rows)) + align256(sizeof(float4) * pieces) +
+  const size_t pieces = static_cast<size_t>(kLogCtas) * sms;
+  return align256(sizeof(int) * (static_cast<size_t>(rows) + 1)) + align256(sizeof(float4) * pieces) +
          sizeof(uint64_t) * kTop * pieces;
 }
 
@@ -608,15 +734,20 @@ int token_logprobs(const void* logits, int logits_type, long long row_stride, in
   p.entropy = entropy;
   p.top_ids = top_ids;
   p.top_logprobs = top_logprobs;
-  p.splits = splits_for(rows, vectors, device_sm_count(device));
-  p.split_vectors = static_cast<int>((vectors + p.splits - 1) / p.splits);
-  const size_t pieces = static_cast<size_t>(rows) * p.splits;
-  if (pieces > 0x7fff0000u) return -EINVAL;
+  const int ctas = kLogCtas * device_sm_count(device);
+  const Cut c = cut(rows, vectors, ctas);
+  p.whole = c.whole;
+  p.splits = c.splits;
+  p.split_vectors = static_cast<int>((vectors + c.splits - 1) / c.splits);
+  const long long pieces = c.whole + static_cast<long long>(rows - c.whole) * c.splits;
+  if (pieces > 0x7fff0000ll) return -EINVAL;
+  p.pieces = static_cast<int>(pieces);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.tickets = reinterpret_cast<int*>(ws);
-  ws += align256(sizeof(int) * static_cast<size_t>(rows));
+  p.counter = reinterpret_cast<int*>(ws);
+  p.tickets = p.counter + 1;
+  ws += align256(sizeof(int) * (static_cast<size_t>(rows) + 1));
   p.sums = reinterpret_cast<float4*>(ws);
-  ws += align256(sizeof(float4) * pieces);
+  ws += align256(sizeof(float4) * static_cast<size_t>(ctas));
   p.keys = reinterpret_cast<uint64_t*>(ws);
   auto kernel = logits_type == PKV_BF16 ? logprobs_kernel<uint16_t> : logprobs_kernel<float>;
   constexpr int kSmem = kLogStages * kStageVectors * 16;
@@ -626,8 +757,7 @@ int token_logprobs(const void* logits, int logits_type, long long row_stride, in
     if (e == cudaSuccess) ready[logits_type].store(true, std::memory_order_relaxed);
   }
   if (e == cudaSuccess) {
-    const size_t most = static_cast<size_t>(kLogCtas) * device_sm_count(device);
-    kernel<<<static_cast<unsigned>(pieces < most ? pieces : most), kLogBlock, kSmem, static_cast<cudaStream_t>(stream)>>>(p);
+    kernel<<<pieces < ctas ? static_cast<int>(pieces) : ctas, kLogBlock, kSmem, static_cast<cudaStream_t>(stream)>>>(p);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) {

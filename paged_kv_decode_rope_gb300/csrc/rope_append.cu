@@ -5,9 +5,10 @@
 // interleaved; with c, s the cos and sin of the token's row of the RoPE table,
 //     y0 = x0 c - x1 s,   y1 = x1 c + x0 s,
 // dims from r on unchanged. q is rotated in fp32 and kept in fp32; k is rounded
-// to bf16 once, exactly as the fp64 rotation rounds it (rotated_bf16_fast
-// certifies the rounding in fp32 double words, rotate_key_dim does it in fp64
-// where it cannot), as every other append of this library; v is copied.
+// to bf16 once, exactly as the fp64 rotation rounds it, as every other append of
+// this library: in fp32 where the result is far enough from a rounding boundary
+// (rotated_bf16_quick, all but about one in two thousand), else in fp32 double
+// words (rotated_bf16_fast), else in fp64. v is copied.
 //
 // The kernel moves (Hq + 2 Hkv) * 128 bytes in and Hq * 256 + Hkv * 256 out a
 // token and computes next to nothing, so memory bounds it, and what it takes
@@ -16,12 +17,10 @@
 // 32 + 8 heads, 42% of the copy bandwidth). So CTAs stay and stream units (a
 // token, up to kUnitRows of its rows) through a ring of kStages shared-memory
 // stages: one warp reads positions and slots ahead and issues bulk copies of
-// the unit's rows and its table row; kRopeWarps warps rotate and store. 16
-// threads hold a head's row, 4 dims (8 bytes of bf16, 16 of fp32) each, so every
-// access is a full row in one go; a thread keeps the same 4 dims of every row.
-// The rotated partner of a dim is in the same thread (interleaved) or in
-// another of the same 16 (half pairs: rot_dim is a multiple of 8, so partners
-// come in whole 4-dim pieces), reached by a shuffle. Every wait is bounded.
+// the unit's rows and its table row; kRopeWarps warps rotate and store. Eight
+// threads hold a head's row, 8 dims each: 4 whole pairs (rot_dim is a multiple
+// of 8), the same ones in every row it takes, or 8 dims that pass through. Every
+// wait is bounded.
 #include <cerrno>
 #include <initializer_list>
 
@@ -32,7 +31,8 @@ namespace pkv {
 namespace {
 
 constexpr int kHalfDim = kHeadDim / 2;
-constexpr int kPieces = kHeadDim / 4;          // threads a row
+constexpr int kPieces = kHeadDim / 8;          // threads a row
+constexpr int kWarpRows = 32 / kPieces;
 constexpr int kRopeWarps = 8;                  // consumers
 constexpr int kRopeThreads = 32 * (kRopeWarps + 1);
 constexpr int kUnitRows = 64;                  // rows of a unit at most
@@ -59,12 +59,29 @@ struct RopeAppendParams {
   int* err;
 };
 
-// One dim of the rotated key in fp64: bf16 of x c - xp s, every operation
-// rounded once.
-__device__ __noinline__ uint16_t rotate_key_dim(float x, float xp, const double2* cs) {
-  const double2 c = *cs;
-  return double_to_bf16_rne(__dsub_rn(__dmul_rn(static_cast<double>(x), c.x),
-                                      __dmul_rn(static_cast<double>(xp), c.y)));
+// a c - b s rounded to bf16 as the exact value rounds, in plain fp32: f has
+// the errors of c and s (2^-24 relative each), of the product a c and of the
+// fma, at most 5 * 2^-24 of the larger product in all, so where the rounding
+// boundary in f's bf16 interval (and the next one, at least 2^-9 |f| away) is
+// farther than 2^-20 of it, f and the exact value round to the same bf16.
+// Returns whether it is (false for zeros, tiny, huge and non-finite values).
+__device__ __forceinline__ bool rotated_bf16_quick(float a, float b, float c, float s, uint32_t& y) {
+  const float pa = __fmul_rn(a, c), f = __fmaf_rn(-b, s, pa);
+  const float m = fmaxf(fabsf(pa), fabsf(__fmul_rn(b, s))), af = fabsf(f);
+  const uint32_t u = __float_as_uint(f);
+  const float mid = __uint_as_float((u & 0x7fff0000u) | 0x8000u);  // same binade as af: exact difference
+  y = (u + 0x8000u) >> 16;
+  return fabsf(__fsub_rn(mid, af)) > __fmul_rn(m, 0x1p-20f) && af >= 0x1p-100f && m <= 0x1p120f &&
+         __fmul_rn(af, 0x1p-10f) > __fmul_rn(m, 0x1p-20f);
+}
+
+// The same where the quick form cannot tell: bf16 of fl64(a c) - fl64(b s).
+__device__ __noinline__ uint32_t rotated_bf16_slow(float a, float b, float4 cs, const double2* cd) {
+  uint16_t y;
+  if (rotated_bf16_fast(a, b, cs.x, cs.y, cs.z, cs.w, y)) return y;
+  const double2 c = *cd;
+  return double_to_bf16_rne(__dsub_rn(__dmul_rn(static_cast<double>(a), c.x),
+                                      __dmul_rn(static_cast<double>(b), c.y)));
 }
 
 template <bool kInterleaved>
@@ -150,13 +167,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(co
         mbar_wait_bounded(smem_addr(&full[k % kRopeStages]), (k / kRopeStages) & 1);
   } else {
     // ---- the consumers ----
-    const int piece = tid % kPieces;  // this thread's dims: 4 piece .. + 3
-    const int half = p.rot_dim / 2;
-    const bool turns = 4 * piece < p.rot_dim;
-    // half pairs: the piece that holds this one's partners, on which side this one is
-    const bool upper = !kInterleaved && 4 * piece >= half;
-    const int partner = (lane & ~(kPieces - 1)) + (!turns ? piece : upper ? piece - half / 4 : piece + half / 4);
-    const int j0 = kInterleaved ? 2 * piece : upper ? 4 * piece - half : 4 * piece;  // its first entry of the table row
+    // This thread's pairs: j0 .. j0 + 3 of the table row; their dims are
+    // d0 .. d0 + 3 and d1 .. d1 + 3 (half pairs), or the eight from d0 on
+    // (interleaved, and where nothing turns).
+    const int piece = tid % kPieces, j0 = 4 * piece;
+    const bool turns = 8 * piece < p.rot_dim, apart = !kInterleaved && turns;
+    const int d0 = apart ? j0 : 8 * piece, d1 = apart ? j0 + p.rot_dim / 2 : d0 + 4;
     int i = 0;
     for (; t < p.tokens; next_unit(), ++i) {
       const int st = i % kRopeStages;
@@ -169,59 +185,67 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(co
       const int n = min(p.unit_rows, rows - r0);
       const uint32_t src = smem_addr(s_ring) + st * kStageBytes;
       const int2 token = s_token[st];
-      float4 cs[4];  // {cos_hi, cos_lo, sin_hi, sin_lo} of each of the thread's dims
+      float4 cs[4];  // {cos_hi, cos_lo, sin_hi, sin_lo} of the thread's pairs
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        cs[e] = turns ? lds128f(src + kUnitRows * kRowBytes + 16 * (j0 + (kInterleaved ? e / 2 : e)))
-                      : make_float4(1.f, 0.f, 0.f, 0.f);
+        cs[e] = turns ? lds128f(src + kUnitRows * kRowBytes + 16 * (j0 + e)) : make_float4(1.f, 0.f, 0.f, 0.f);
       uint16_t* page = p.pool +
                        static_cast<size_t>(max(token.y, 0) / kPage) * p.hkv * (kHeadPageBytes / 2) +
-                       (max(token.y, 0) % kPage) * kHeadDim + 4 * piece;
-      // two rows a warp; the warps take turns, so that the key rows, ten times
-      // the work of the others, do not always fall to the same ones
-      for (int r = 2 * ((warp + 4 * i) % kRopeWarps); r < n; r += 2 * kRopeWarps) {
+                       (max(token.y, 0) % kPage) * kHeadDim;
+      // kWarpRows rows a warp; the warps take turns, so that the key rows, the
+      // most work, do not always fall to the same ones
+      for (int r = kWarpRows * ((warp + 4 * i) % kRopeWarps); r < n; r += kWarpRows * kRopeWarps) {
         const int local = r + lane / kPieces, row = r0 + local;
-        const uint2 w = lds64u(src + min(local, n - 1) * kRowBytes + 8 * piece);
-        float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
-        const float own[4] = {a.x, a.y, b.x, b.y};
-        float other[4];  // what each dim's sin multiplies, with its sign: y = own cos - other sin
-        if (kInterleaved) {
-          other[0] = own[1];
-          other[1] = -own[0];
-          other[2] = own[3];
-          other[3] = -own[2];
-        } else {
-          a = bf16x2_to_float2(__shfl_sync(kFull, w.x, partner));
-          b = bf16x2_to_float2(__shfl_sync(kFull, w.y, partner));
-          other[0] = upper ? -a.x : a.x;
-          other[1] = upper ? -a.y : a.y;
-          other[2] = upper ? -b.x : b.x;
-          other[3] = upper ? -b.y : b.y;
-        }
         if (local >= n) continue;
-        if (row < p.hq) {
-          float y[4];
+        const uint2 w0 = lds64u(src + local * kRowBytes + 2 * d0), w1 = lds64u(src + local * kRowBytes + 2 * d1);
+        float a[4], b[4];  // the pairs' first and second dims
+        {
+          const float2 f0 = bf16x2_to_float2(w0.x), f1 = bf16x2_to_float2(w0.y);
+          const float2 f2 = bf16x2_to_float2(w1.x), f3 = bf16x2_to_float2(w1.y);
+          const float x[8] = {f0.x, f0.y, f1.x, f1.y, f2.x, f2.y, f3.x, f3.y};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            y[e] = turns ? own[e] * cs[e].x - other[e] * cs[e].z : own[e];
-            if (token.x < 0) y[e] = 0.f;
+            a[e] = kInterleaved ? x[2 * e] : x[e];
+            b[e] = kInterleaved ? x[2 * e + 1] : x[4 + e];
           }
-          *reinterpret_cast<float4*>(p.q_rot + (static_cast<size_t>(t) * p.hq + row) * kHeadDim + 4 * piece) =
-              make_float4(y[0], y[1], y[2], y[3]);
+        }
+        if (row < p.hq) {
+          float y[8];  // dims d0 .. + 3, d1 .. + 3
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float y0 = a[e] * cs[e].x - b[e] * cs[e].z, y1 = b[e] * cs[e].x + a[e] * cs[e].z;
+            if (!turns) {
+              y0 = a[e];
+              y1 = b[e];
+            }
+            if (token.x < 0) y0 = y1 = 0.f;
+            y[kInterleaved ? 2 * e : e] = y0;
+            y[kInterleaved ? 2 * e + 1 : 4 + e] = y1;
+          }
+          float* dst = p.q_rot + (static_cast<size_t>(t) * p.hq + row) * kHeadDim;
+          *reinterpret_cast<float4*>(dst + d0) = make_float4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<float4*>(dst + d1) = make_float4(y[4], y[5], y[6], y[7]);
         } else if (token.y >= 0) {
           const bool key = row < p.hq + p.hkv;
           const int h = row - p.hq - (key ? 0 : p.hkv);
-          uint2 out = w;
+          uint2 o0 = w0, o1 = w1;
           if (key && turns) {
-            uint16_t y[4];
+            uint32_t y[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!rotated_bf16_fast(own[e], other[e], cs[e].x, cs[e].y, cs[e].z, cs[e].w, y[e]))
-                y[e] = rotate_key_dim(own[e], other[e],
-                                      p.rope_dd + static_cast<size_t>(token.x) * kHalfDim + j0 + (kInterleaved ? e / 2 : e));
-            out = make_uint2(y[0] | static_cast<uint32_t>(y[1]) << 16, y[2] | static_cast<uint32_t>(y[3]) << 16);
+            for (int e = 0; e < 4; ++e) {
+              const double2* cd = p.rope_dd + static_cast<size_t>(token.x) * kHalfDim + j0 + e;
+              uint32_t y0, y1;
+              if (!rotated_bf16_quick(a[e], b[e], cs[e].x, cs[e].z, y0)) y0 = rotated_bf16_slow(a[e], b[e], cs[e], cd);
+              if (!rotated_bf16_quick(b[e], -a[e], cs[e].x, cs[e].z, y1)) y1 = rotated_bf16_slow(b[e], -a[e], cs[e], cd);
+              y[kInterleaved ? 2 * e : e] = y0;
+              y[kInterleaved ? 2 * e + 1 : 4 + e] = y1;
+            }
+            o0 = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
+            o1 = make_uint2(y[4] | y[5] << 16, y[6] | y[7] << 16);
           }
-          *reinterpret_cast<uint2*>(page + (h * 2 + (key ? 0 : 1)) * (kHalfBytes / 2)) = out;
+          uint16_t* dst = page + (h * 2 + (key ? 0 : 1)) * (kHalfBytes / 2);
+          *reinterpret_cast<uint2*>(dst + d0) = o0;
+          *reinterpret_cast<uint2*>(dst + d1) = o1;
         }
       }
       __syncwarp();  // this warp has read the stage
