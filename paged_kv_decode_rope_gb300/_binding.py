@@ -1,12 +1,15 @@
 """ctypes binding of the pkv C ABI (include/pkv.h).
 
 Argument marshalling only: shapes and pointers are read off torch tensors and
-passed to the CUDA library, which does all of the work on the device. There is
-no fallback: if libpkv.so is missing or fails to load, every call raises.
+passed to the CUDA library, which does all of the work on the device (the
+calls of a serving step through a CPython module, csrc/host/pkv_call.cpp, the
+others through ctypes). There is no fallback: if libpkv.so is missing or fails
+to load, every call raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -77,9 +80,6 @@ _SIGNATURES = {
 class _Scoring(ctypes.Structure):
     """pkv_scoring_t."""
     _fields_ = [("scale", _f), ("softcap", _f), ("alibi_slopes", _vp), ("window", _i)]
-
-
-_TYPES = {torch.bfloat16: 0, torch.float32: 1}  # PKV_BF16, PKV_F32
 
 
 class PkvError(RuntimeError):
@@ -457,58 +457,35 @@ def paged_kv_split_combine(o_part: torch.Tensor, lse_part: torch.Tensor, num_spl
     _check("paged_kv_split_combine", rc)
 
 
-# A small step's calls last no longer on the GPU than their checks take here
-# (about 0.4 us a tensor), so these check a tensor once, in the order that ends
-# soonest, and leave the wording of a refusal to _shape and _dev.
+# The calls of a serving step take 2 to 4 us of GPU time on a small one; checked
+# here and passed through ctypes they took 8 to 11 us. Their checks and calls are
+# in csrc/host/pkv_call.cpp.
+_call_module = None
 
 
-def _arg(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str) -> int:
-    """The pointer of a contiguous CUDA tensor of exactly this type and shape."""
-    try:
-        if t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:  # not a tensor
-        pass
-    _shape(t, shape, name)
-    return _dev(t, dtype, name)
+def _native():
+    global _call_module
+    with _lock:
+        if _call_module is not None:
+            return _call_module
+    L = lib()
+    path = os.path.join(_HERE, "_pkv_call.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is not built; run paged_kv_decode_rope_gb300.build.build()")
+    spec = importlib.util.spec_from_file_location("_pkv_call", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(L, name), _vp).value for name in
+                  ("paged_tables_build", "paged_rope_append", "paged_gqa_decode_scored", "paged_gqa_prefill_scored",
+                   "token_logprobs")))
+    _call_module = module
+    return module
 
 
-def _sizes(t: torch.Tensor, ndim: int, name: str) -> tuple:
-    """The shape of a tensor of ndim dimensions."""
-    try:
-        shape = t.shape
-        if len(shape) == ndim:
-            return shape
-    except AttributeError:
-        pass
-    return _shape(t, (None,) * ndim, name)
-
-
-def _bytes(t: torch.Tensor, name: str) -> int:
-    """The pointer of a contiguous uint8 CUDA tensor (a workspace, a table)."""
-    try:
-        if t.dtype is torch.uint8 and t.is_cuda and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    return _dev(t, torch.uint8, name)
-
-
-def _optional(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, name: str) -> int | None:
-    return None if t is None else _arg(t, dtype, shape, name)
-
-
-def _raw_stream(stream, t: torch.Tensor) -> int:
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else _stream(stream)
-
-
-def _typed(t: torch.Tensor, name: str) -> int:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    try:
-        return _TYPES[t.dtype]
-    except KeyError:
-        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}") from None
+def _refused(fn: str, rc: int, pool: KVPool | None = None) -> None:
+    if pool is not None:
+        pool.handle  # a destroyed pool says so
+    raise PkvError(fn, rc)
 
 
 def paged_tables_build(pool: KVPool, start_pos: torch.Tensor, new_tokens: torch.Tensor,
@@ -520,20 +497,11 @@ def paged_tables_build(pool: KVPool, start_pos: torch.Tensor, new_tokens: torch.
     block_tables [L,B,max_blocks] int32 in and out; free_head_out [1] (not
     free_head itself), cu_tokens [B+1], seq_lens [B], positions [T],
     slot_map [L,T] int32 out, T the capacity in tokens."""
-    i32 = torch.int32
-    tables = layers, batch, max_blocks = _sizes(block_tables, 3, "block_tables")
-    (capacity,) = tokens = _sizes(positions, 1, "positions")
-    (num_free,) = free = _sizes(free_pages, 1, "free_pages")
-    rc = (_lib or lib()).paged_tables_build(
-        pool.handle, _arg(start_pos, i32, (batch,), "start_pos"), _arg(new_tokens, i32, (batch,), "new_tokens"),
-        batch, layers, _arg(free_pages, i32, free, "free_pages"), num_free,
-        _arg(free_head, i32, (1,), "free_head"), _arg(free_head_out, i32, (1,), "free_head_out"),
-        _arg(block_tables, i32, tables, "block_tables"), max_blocks,
-        _arg(cu_tokens, i32, (batch + 1,), "cu_tokens"), _arg(seq_lens, i32, (batch,), "seq_lens"),
-        _arg(positions, i32, tokens, "positions"), _arg(slot_map, i32, (layers, capacity), "slot_map"),
-        capacity, _raw_stream(stream, block_tables))
+    rc = (_call_module or _native()).paged_tables_build(
+        pool._handle or 0, start_pos, new_tokens, free_pages, free_head, free_head_out, block_tables, cu_tokens,
+        seq_lens, positions, slot_map, stream)
     if rc:
-        raise PkvError("paged_tables_build", rc)
+        _refused("paged_tables_build", rc, pool)
 
 
 def paged_rope_table_build_freqs(inv_freq, num_positions: int, table: torch.Tensor, magnitude: float = 1.0,
@@ -550,21 +518,6 @@ def paged_rope_table_build_freqs(inv_freq, num_positions: int, table: torch.Tens
     _check("paged_rope_table_build_freqs", rc)
 
 
-def _token_rows(t: torch.Tensor, tokens: int, heads: int, name: str) -> tuple[int, int]:
-    """Pointer and token stride (elements) of bf16 [tokens][heads][64] whose
-    heads are contiguous: the whole tensor, or a slice of a projection."""
-    if _sizes(t, 3, name) != (tokens, heads, HEAD_DIM):
-        _shape(t, (tokens, heads, HEAD_DIM), name)
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype is not torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    stride, head, dim = t.stride()
-    if (dim != 1 or (head != HEAD_DIM and heads > 1)) and tokens > 0:
-        raise ValueError(f"{name} must have contiguous heads")
-    return t.data_ptr(), stride if tokens > 1 else heads * HEAD_DIM
-
-
 def paged_rope_append(pool: KVPool, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_rot: torch.Tensor,
                       slot_map: torch.Tensor, positions: torch.Tensor, rope_table: torch.Tensor,
                       rot_dim: int = HEAD_DIM, interleaved: bool = False, stream=None) -> None:
@@ -573,23 +526,11 @@ def paged_rope_append(pool: KVPool, q: torch.Tensor, k: torch.Tensor, v: torch.T
     [T] int32 (one layer's slots; negative: not stored). q_rot [T,Hq,64] fp32
     out; positions [T] int32, rows of rope_table. q, k and v may be slices of
     one projection's output (any token stride)."""
-    tokens, hq, _ = _sizes(q, 3, "q")
-    hkv = pool.num_kv_heads
-    qp, qs = _token_rows(q, tokens, hq, "q")
-    kp, ks = _token_rows(k, tokens, hkv, "k")
-    vp, vs = _token_rows(v, tokens, hkv, "v")
-    rc = (_lib or lib()).paged_rope_append(
-        pool.handle, qp, qs, kp, ks, vp, vs, _arg(q_rot, torch.float32, (tokens, hq, HEAD_DIM), "q_rot"),
-        _arg(slot_map, torch.int32, (tokens,), "slot_map"), _arg(positions, torch.int32, (tokens,), "positions"),
-        tokens, hq, _bytes(rope_table, "rope_table"), rope_table.numel() // ROPE_TABLE_BYTES_PER_ROW, int(rot_dim),
-        1 if interleaved else 0, _raw_stream(stream, q))
+    rc = (_call_module or _native()).paged_rope_append(
+        pool._handle or 0, pool.num_kv_heads, q, k, v, q_rot, slot_map, positions, rope_table, rot_dim, interleaved,
+        stream)
     if rc:
-        raise PkvError("paged_rope_append", rc)
-
-
-def _scoring(scale, softcap, alibi_slopes, window, hq):
-    return ctypes.byref(_Scoring(scale, softcap, _optional(alibi_slopes, torch.float32, (hq,), "alibi_slopes"),
-                                 window))
+        _refused("paged_rope_append", rc, pool)
 
 
 def paged_gqa_decode_scored(pool: KVPool, q_rot: torch.Tensor, out: torch.Tensor, block_tables: torch.Tensor,
@@ -600,18 +541,11 @@ def paged_gqa_decode_scored(pool: KVPool, q_rot: torch.Tensor, out: torch.Tensor
     (alibi_slopes [Hq] fp32) and windowed (window > 0) scores, over keys from
     first_keys [B] int32 on. q_rot [B,Hq,64] fp32, out [B,Hq,64] fp32 or
     bf16; workspace from alloc_decode_workspace()."""
-    batch, hq, _ = _sizes(q_rot, 3, "q_rot")
-    _, max_blocks = _sizes(block_tables, 2, "block_tables")
-    rows = (batch, hq, HEAD_DIM)
-    out_type = _typed(out, "out")
-    rc = (_lib or lib()).paged_gqa_decode_scored(
-        pool.handle, _arg(q_rot, torch.float32, rows, "q_rot"), _arg(out, out.dtype, rows, "out"), out_type,
-        _arg(block_tables, torch.int32, (batch, max_blocks), "block_tables"), max_blocks,
-        _arg(seq_lens, torch.int32, (batch,), "seq_lens"), _optional(first_keys, torch.int32, (batch,), "first_keys"),
-        batch, hq, _scoring(scale, softcap, alibi_slopes, window, hq), _bytes(workspace, "workspace"),
-        workspace.numel(), _raw_stream(stream, q_rot))
+    rc = (_call_module or _native()).paged_gqa_decode_scored(
+        pool._handle or 0, q_rot, out, block_tables, seq_lens, scale, workspace, softcap, alibi_slopes, window,
+        first_keys, stream)
     if rc:
-        raise PkvError("paged_gqa_decode_scored", rc)
+        _refused("paged_gqa_decode_scored", rc, pool)
 
 
 def paged_gqa_prefill_scored(pool: KVPool, q_rot: torch.Tensor, out: torch.Tensor, block_tables: torch.Tensor,
@@ -627,20 +561,11 @@ def paged_gqa_prefill_scored(pool: KVPool, q_rot: torch.Tensor, out: torch.Tenso
     q_rot [T,Hq,64] fp32, out [T,Hq,64] fp32 or bf16, block_tables
     [B,max_blocks], cu_tokens [B+1], start_pos [B] int32; workspace from
     alloc_prefill_workspace()."""
-    total, hq, _ = _sizes(q_rot, 3, "q_rot")
-    tables = batch, max_blocks = _sizes(block_tables, 2, "block_tables")
-    rows = (total, hq, HEAD_DIM)
-    i32 = torch.int32
-    out_type = _typed(out, "out")
-    rc = (_lib or lib()).paged_gqa_prefill_scored(
-        pool.handle, _arg(q_rot, torch.float32, rows, "q_rot"), _arg(out, out.dtype, rows, "out"), out_type,
-        _arg(block_tables, i32, tables, "block_tables"), max_blocks,
-        _arg(cu_tokens, i32, (batch + 1,), "cu_tokens"), _arg(start_pos, i32, (batch,), "start_pos"),
-        _optional(prefix_lens, i32, (batch,), "prefix_lens"), _optional(doc_starts, i32, (total,), "doc_starts"),
-        batch, total, hq, _scoring(scale, softcap, alibi_slopes, window, hq),
-        _bytes(workspace, "workspace"), workspace.numel(), _raw_stream(stream, q_rot))
+    rc = (_call_module or _native()).paged_gqa_prefill_scored(
+        pool._handle or 0, q_rot, out, block_tables, cu_tokens, start_pos, scale, workspace, softcap, alibi_slopes,
+        window, prefix_lens, doc_starts, stream)
     if rc:
-        raise PkvError("paged_gqa_prefill_scored", rc)
+        _refused("paged_gqa_prefill_scored", rc, pool)
 
 
 def token_logprobs_workspace_bytes(rows: int, vocab: int, top: int) -> int:
@@ -665,22 +590,10 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None, logprobs:
     entropy [R] fp32 of each row; its K most likely tokens top_ids [R,K] int32
     with top_logprobs [R,K] fp32 (K up to 32, the lower id first among
     equals). Outputs that are None are left out."""
-    rows, vocab = _sizes(logits, 2, "logits")
-    if not logits.is_cuda:
-        raise ValueError("logits must be a CUDA tensor")
-    stride, step = logits.stride()
-    if step != 1 and vocab > 1:
-        raise ValueError("logits must have contiguous rows")
-    top = 0 if top_ids is None else _sizes(top_ids, 2, "top_ids")[1]
-    f32, i32 = torch.float32, torch.int32
-    rc = (_lib or lib()).token_logprobs(
-        logits.data_ptr(), _typed(logits, "logits"), stride if rows > 1 else vocab, rows, vocab, scale,
-        _optional(targets, i32, (rows,), "targets"), top, _optional(logprobs, f32, (rows,), "logprobs"),
-        _optional(entropy, f32, (rows,), "entropy"), _optional(top_ids, i32, (rows, top), "top_ids"),
-        _optional(top_logprobs, f32, (rows, top), "top_logprobs"), _bytes(workspace, "workspace"),
-        workspace.numel(), _raw_stream(stream, logits))
+    rc = (_call_module or _native()).token_logprobs(logits, targets, logprobs, entropy, top_ids, top_logprobs,
+                                                    workspace, scale, stream)
     if rc:
-        raise PkvError("token_logprobs", rc)
+        _refused("token_logprobs", rc)
 
 
 def pkv_get_error(pool: KVPool, reset: bool = False) -> int:

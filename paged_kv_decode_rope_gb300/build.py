@@ -1,8 +1,10 @@
 """Build the pkv CUDA library (libpkv.so) in-tree for sm_103a.
 
 Each translation unit is compiled in parallel with nvcc, then linked into one
-shared library next to this file. Rebuilds only when a source is newer than
-the library.
+shared library next to this file. Beside it the CPython module _pkv_call.so
+(csrc/host/pkv_call.cpp, the argument checks of the serving calls) is built with
+the host compiler against the installed torch. Rebuilds only when a source is
+newer than what it makes.
 """
 from __future__ import annotations
 
@@ -16,6 +18,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIBRARY = os.path.join(HERE, "libpkv.so")
+CALL_SOURCE = os.path.join(CSRC, "host", "pkv_call.cpp")
+CALL_MODULE = os.path.join(HERE, "_pkv_call.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -46,8 +50,33 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def build_call(force: bool = False) -> str:
+    """The CPython module, against the Python and torch that run this."""
+    inputs = [CALL_SOURCE, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(CALL_MODULE) and \
+            all(os.path.getmtime(f) <= os.path.getmtime(CALL_MODULE) for f in inputs):
+        return CALL_MODULE
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+               os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")]
+    tmp = CALL_MODULE + f".{os.getpid()}.tmp"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in include),
+           CALL_SOURCE, "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiler failed for {CALL_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL_MODULE)
+    return CALL_MODULE
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     if not force and up_to_date():
+        build_call()
         return LIBRARY
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -63,8 +92,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(r.stdout + r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(sources())) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(sources()) + 1) as ex:
+        module = ex.submit(build_call, force)
         objs = list(ex.map(compile_one, sources()))
+        module.result()
     tmp = LIBRARY + f".{os.getpid()}.tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
