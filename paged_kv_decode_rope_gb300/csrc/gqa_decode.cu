@@ -1453,6 +1453,7 @@ cudaError_t launch_plan(const int32_t* seq_lens, const int32_t* positions, int r
 
 cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream) {
   if (a.batch == 0) return cudaSuccess;
+  if (a.scored && decode_small_fits(a)) return launch_decode_small(a, stream);
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;

@@ -142,6 +142,9 @@ constexpr int kDecodeBatchChunk = 2048;
 size_t decode_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int max_blocks,
                               int pages_per_split, int sm_count);
 cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream);
+// The scored decode for little work (decode_small.cu), and whether this is little.
+bool decode_small_fits(const DecodeLaunch& a);
+cudaError_t launch_decode_small(const DecodeLaunch& a, cudaStream_t stream);
 // The step's work plan in the decode workspace (positions null: for the
 // decode from q_rot, whose lengths are not checked against positions).
 cudaError_t launch_plan(const int32_t* seq_lens, const int32_t* positions, int rope_positions,

@@ -122,33 +122,45 @@ def run_decode(seed, hq, hkv, lens, softcap=0.0, alibi=False, window=0, first=No
 
 LENS = [1, 2, 15, 16, 17, 33, 160, 700]
 
+# Block tables that could hold long sequences (1100 pages) take the general
+# kernel, narrow ones the kernel for little work.
+WIDE = pytest.mark.parametrize("max_blocks", [None, 1100], ids=["narrow", "wide"])
+
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("hq,hkv", [(32, 8), (14, 2), (3, 3), (8, 1), (15, 5), (6, 3), (10, 2), (12, 2)])
 @pytest.mark.parametrize("softcap,alibi,window", [(0.0, False, 0), (20.0, False, 0), (0.0, True, 0), (5.0, True, 40)])
-def test_decode_groups_and_scores(hq, hkv, softcap, alibi, window):
-    run_decode(hq + window, hq, hkv, LENS, softcap, alibi, window)
+@WIDE
+def test_decode_groups_and_scores(hq, hkv, softcap, alibi, window, max_blocks):
+    run_decode(hq + window, hq, hkv, LENS, softcap, alibi, window, max_blocks=max_blocks)
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 31, 100, 699, 700, 5000, 2**31 - 1])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-def test_decode_windows(window, dtype):
-    run_decode(window % 1000, 8, 2, LENS, 30.0, True, window, dtype=dtype)
+@WIDE
+def test_decode_windows(window, dtype, max_blocks):
+    # (a window bounds the pages that count: many sequences take the general kernel with it)
+    run_decode(window % 1000, 8, 2, LENS * (1 if max_blocks is None else 60), 30.0, True, window, dtype=dtype,
+               max_blocks=max_blocks)
 
 
 @pytest.mark.gpu
-def test_decode_first_keys_and_rows_that_see_nothing():
-    run_decode(1, 8, 4, LENS, 0.0, False, 0, first=[0, -5, 3, 16, 16, 32, 100, 2**31 - 1])
+@WIDE
+def test_decode_first_keys_and_rows_that_see_nothing(max_blocks):
+    run_decode(1, 8, 4, LENS, 0.0, False, 0, first=[0, -5, 3, 16, 16, 32, 100, 2**31 - 1], max_blocks=max_blocks)
+    run_decode(2, 8, 4, LENS, 10.0, True, 0, first=[1, 5, 14, 15, 0, 31, 1000, 690], dtype=torch.bfloat16,
+               max_blocks=max_blocks)
     run_decode(2, 8, 4, LENS, 10.0, True, 20, first=[1, 5, 14, 15, 0, 31, 1000, 690], dtype=torch.bfloat16)
-    run_decode(3, 8, 4, [9, 40], first=[9, 40])  # all rows empty
+    run_decode(3, 8, 4, [9, 40], first=[9, 40], max_blocks=max_blocks)  # all rows empty
 
 
 @pytest.mark.gpu
 def test_decode_one_long_sequence_and_many_short_ones():
     run_decode(4, 32, 8, [9000], 50.0, False, 0)
     run_decode(5, 14, 2, [20000, 3], 0.0, True, 0, dtype=torch.bfloat16)
-    run_decode(6, 4, 2, [1 + (7 * i) % 37 for i in range(1100)], 50.0, False, 8)  # more than one launch
+    run_decode(6, 4, 2, [1 + (7 * i) % 37 for i in range(1100)], 50.0, False, 8)
+    run_decode(6, 4, 2, [1 + (7 * i) % 37 for i in range(1100)], 50.0, True, 0, max_blocks=1100)  # two launches
 
 
 @pytest.mark.gpu
@@ -156,26 +168,30 @@ def test_decode_without_scoring_is_the_plain_decode():
     rng = np.random.default_rng(7)
     lens = [5, 300, 1200]
     tables, pool = spread(rng, [(0, -(-n // PAGE)) for n in lens], 80, 8)
-    for b, n in enumerate(lens):
-        fill(rng, pool, tables, b, 0, n)
+    kv = [fill(rng, pool, tables, b, 0, n) for b, n in enumerate(lens)]
     handle = pkv.kv_pool_create(pool.cuda(), 8)
     q = torch.from_numpy(rng.standard_normal((3, 32, D))).float().cuda()
     ws = pkv.alloc_decode_workspace(3, 32, 8, 80)
     a, b = torch.empty_like(q), torch.empty_like(q)
     tables = torch.tensor(tables, dtype=torch.int32, device="cuda")
-    lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
-    pkv.paged_gqa_decode(handle, q, a, tables, lens, SCALE, ws)
-    pkv.paged_gqa_decode_scored(handle, q, b, tables, lens, SCALE, ws)
-    torch.cuda.synchronize()
-    assert torch.equal(a, b)
+    dev_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    pkv.paged_gqa_decode(handle, q, a, tables, dev_lens, SCALE, ws)
+    pkv.paged_gqa_decode_scored(handle, q, b, tables, dev_lens, SCALE, ws)
+    assert pkv.pkv_get_error(handle) == 0
+    # (not the same bits: few sequences take a kernel of their own)
+    for i, n in enumerate(lens):
+        want, tol = reference(q[i:i + 1].double().cpu().numpy(), *kv[i], [n - 1], [0], [n], 0.0, None)
+        compare(a[i:i + 1], want, tol, torch.float32)
+        compare(b[i:i + 1], want, tol, torch.float32)
     handle.close()
 
 
 @pytest.mark.gpu
-def test_decode_bad_lengths_and_pages():
+@pytest.mark.parametrize("max_blocks", [4, 1100], ids=["narrow", "wide"])
+def test_decode_bad_lengths_and_pages(max_blocks):
     rng = np.random.default_rng(8)
-    lens = [40, 0, -3, 1000, 20]
-    tables, pool = spread(rng, [(0, 3), (0, 0), (0, 0), (0, 0), (0, 2)], 4, 2)
+    lens = [40, 0, -3, 16 * max_blocks + 1, 20]
+    tables, pool = spread(rng, [(0, 3), (0, 0), (0, 0), (0, 0), (0, 2)], max_blocks, 2)
     k, v = fill(rng, pool, tables, 0, 0, 40)
     k4, v4 = fill(rng, pool, tables, 4, 0, 20)
     tables[0, 1] = 10**6  # a bad page: its keys are skipped
@@ -184,7 +200,7 @@ def test_decode_bad_lengths_and_pages():
     out = torch.full((5, 8, D), float("nan"), dtype=torch.bfloat16, device="cuda")
     i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")  # noqa: E731
     pkv.paged_gqa_decode_scored(handle, q.cuda(), out, i32(tables), i32(lens), SCALE,
-                                pkv.alloc_decode_workspace(5, 8, 2, 4), softcap=9.0)
+                                pkv.alloc_decode_workspace(5, 8, 2, max_blocks), softcap=9.0)
     assert pkv.pkv_get_error(handle) == pkv.ERR_SEQ_LEN | pkv.ERR_PAGE_ID
     assert (out[1:4] == 0).all()
     keep = np.r_[0:16, 32:40]
