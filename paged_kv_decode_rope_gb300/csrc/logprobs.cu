@@ -296,6 +296,10 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
   }
   fence_mbar_init();
   __syncthreads();
+  // The launch overlaps the end of the kernel before it, and the next one's
+  // this one's end; logits, workspace and outputs are touched from here on.
+  grid_launch_dependents();
+  grid_dependency_wait();
   int chunk = 0;  // stages used so far
 
   if (warp == kLogWarps) {
@@ -757,8 +761,17 @@ int token_logprobs(const void* logits, int logits_type, long long row_stride, in
     if (e == cudaSuccess) ready[logits_type].store(true, std::memory_order_relaxed);
   }
   if (e == cudaSuccess) {
-    kernel<<<pieces < ctas ? static_cast<int>(pieces) : ctas, kLogBlock, kSmem, static_cast<cudaStream_t>(stream)>>>(p);
-    e = cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(pieces < ctas ? pieces : ctas));
+    cfg.blockDim = dim3(kLogBlock);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, p);
   }
   if (e != cudaSuccess) {
     record_cuda_error(e);

@@ -12,13 +12,15 @@
 // head (row R = token R / G, head R % G): the M = 128 of one tcgen05 MMA. Keys
 // go in steps of 64 (four pages) from the page of the tile's first visible key
 // to its last. Per step:
-//   S = Q_hi K^T + Q_lo K^T          (tensor memory, 128 x 64 fp32, three buffers)
+//   S = Q_hi K^T + Q_lo K^T          (tensor memory, 128 x 64 fp32, two buffers)
 //   softmax warps: P = exp2(S - m)   row R = tensor-memory lane R
 //   O += P V (+ P_lo V)              (tensor memory, 128 x 64 fp32; P over its own S)
+//   l += P 1                         (tensor memory; the row sums, as a product with a tile of ones)
 // Q enters as bf16 plus its bf16 rounding remainder (about 16 bits), as
 // everywhere in this library, and so does P where the output is fp32 (kPair).
-// Where the output is bf16, P is rounded to bf16 once: the row sum is taken of
-// the rounded P, so the weights still sum to one, and what is left (1.1 to 1.35
+// Where the output is bf16, P is rounded to bf16 once, and the tensor core sums
+// the rounded P, so that the weights still sum to one (and no instruction of the
+// softmax is spent on the sums); what is left (1.1 to 1.35
 // times the error of rounding the output alone, over 16 to 2048 keys) costs a
 // quarter less of the softmax's arithmetic and half the P V products. Scores,
 // sums and O are fp32. The
@@ -54,8 +56,8 @@ namespace {
 
 constexpr float kSlack = 8.f;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kSBufs = 3;
-constexpr uint32_t kTmemCols = 256;  // three S buffers of 64 columns, O
+constexpr int kSBufs = 2;
+constexpr uint32_t kTmemCols = 256;  // two S buffers of 64 columns, O (64), l (16 equal columns)
 constexpr int kCtas = 2;             // CTAs a SM
 
 // tanh(x) on |x| <= kPolyMax as x (c0 + c1 x^2 + c2 x^4) with the smallest
@@ -110,10 +112,11 @@ struct Cfg {
                 "the register shares exceed what two CTAs an SM give a CTA");
   static constexpr uint32_t kTile = 128 * 128;  // a 128-row x 128-byte operand tile
   static constexpr uint32_t kStep = 64 * 128;   // 64 K rows (or V rows) of one step
-  // dynamic shared memory: Q_hi, Q_lo, then per stage K and V
+  // dynamic shared memory: Q_hi, Q_lo, per stage K and V, then 16 rows of ones
   static constexpr uint32_t kQhi = 0, kQlo = kTile;
   static constexpr uint32_t kStage0 = 2 * kTile;
-  static constexpr uint32_t kBytes = kStage0 + kStages * 2 * kStep;
+  static constexpr uint32_t kOnes = kStage0 + kStages * 2 * kStep;
+  static constexpr uint32_t kBytes = kOnes + 16 * 128;
 };
 
 template <int G, bool kPair>
@@ -145,8 +148,8 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
       mbar_init(smem_addr(&v_empty[st]), 1);
     }
     mbar_init(smem_addr(&q_ready), C::kSoftmaxThreads);
-    // S done, P ready and P V done, one barrier each per buffer (step % 3): a
-    // wait for a step never sees its barrier two phases on
+    // S done, P ready and P V done, one barrier each per buffer (step % kSBufs):
+    // a wait for a step never sees its barrier two phases on
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(smem_addr(&s_full[i]), 1);
       mbar_init(smem_addr(&p_full[i]), C::kSoftmaxThreads);
@@ -158,13 +161,16 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
       mbar_init(smem_addr(&tile_empty[i]), 11);  // every warp but the key warp
     }
   }
+  for (int i = tid; i < 16 * 128 / 4; i += C::kThreads)
+    reinterpret_cast<uint32_t*>(gbase + C::kOnes)[i] = 0x3F803F80u;  // (the same in any swizzle)
+  fence_proxy_async_smem();
   fence_mbar_init();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   // The plan is the kernel before this one: the set-up overlaps its end.
   grid_dependency_wait();
-  const uint32_t tmem = s_tmem, tO = tmem + 64 * kSBufs;
+  const uint32_t tmem = s_tmem, tO = tmem + 64 * kSBufs, tL = tO + 64;
   // steps are numbered through, tile after tile
   auto tS = [&](int g) { return tmem + 64 * (g % kSBufs); };  // S, then P (hi: +0, lo: +32)
   auto buf = [](int g) { return g % kSBufs; };
@@ -345,6 +351,8 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
         return __all_sync(kFull, mbar_wait_idle(bar, parity)) != 0;
       };
       constexpr uint32_t idS = idesc_bf16_f32(128, 64, false), idPV = idesc_bf16_f32(128, 64, true);
+      constexpr uint32_t idL = idesc_bf16_f32(128, 16, false);
+      const uint64_t dOnes = smem_desc_sw128(base + C::kOnes);
       const uint64_t dQhi = smem_desc_sw128(base + C::kQhi), dQlo = smem_desc_sw128(base + C::kQlo);
       int g = 0;
       for (int n = 0; !failed; ++n) {
@@ -359,7 +367,7 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
           if (!wait_all(smem_addr(&q_ready), n & 1)) failed = true;
           for (int j = 0; j < n_steps && !failed; ++j, ++g) {
             const int st = g % C::kStages;
-            // S goes into the buffer of the P three steps before: once its P V is done
+            // S goes into the buffer of the P kSBufs steps before: once its P V is done
             if (g >= kSBufs && !wait_all(smem_addr(&pv_done[buf(g)]), par(g - kSBufs))) failed = true;
             if (failed || !wait_all(smem_addr(&k_full[st]), (g / C::kStages) & 1)) {
               failed = true;
@@ -393,6 +401,9 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
             if constexpr (kPair) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) umma_bf16_tmem_a(tO, tS(g) + 32 + 8 * k, dV + 128 * k, idPV, true);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) umma_bf16_tmem_a(tL, tS(g) + 8 * k, dOnes + 2 * k, idL, j > 0 || k > 0);
             }
             umma_commit(smem_addr(&v_empty[st]));
             umma_commit(smem_addr(&pv_done[buf(g)]));
@@ -486,7 +497,11 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
     for (; some && !failed; ++n) {
       const Tile& t = s_tile[n & 1];
       const int n_steps = t.n_steps;
-      float m_ref[2] = {-INFINITY, -INFINITY}, l_sum[2] = {0.f, 0.f};
+      // the rows' references (0 until a row has seen a key: `set`), and with
+      // kPair their sums
+      float m_ref[2] = {0.f, 0.f};
+      [[maybe_unused]] float l_sum[2] = {0.f, 0.f};
+      bool set[2] = {false, false};
       // which pages have a bad id: bit i of bad_win for page window_page(m) + i,
       // the next window loaded while this one is used
       auto bad_bits = [&](int id, int m) {
@@ -510,9 +525,26 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
         const int bad = static_cast<int>((bad_win >> window_lane(j)) & 0xFu);
         if (!mbar_wait_bounded(smem_addr(&s_full[buf(g)]), par(g))) failed = true;
         tc_fence_after();
-        // S, capped and biased, with the keys that get no weight at -inf
+        // S, capped and biased, less the row's reference as it stands, with the
+        // keys that get no weight at -inf
         float sv[32];
-        float shift[2] = {0.f, 0.f};  // what this thread's scores of a row still lack
+        // what is taken off this thread's scores of each row: the reference less
+        // the part of the bias that is common to the step
+        uint64_t off[2];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float x = -m_ref[hh];
+          if (p.slopes && !p.prefix_lens) x += slope[hh] * static_cast<float>(kb - pos[hh]);
+          off[hh] = f32x2(x, x);
+        }
+        auto take_off = [&]() {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 v = unpack_f32x2(add_f32x2(f32x2(sv[2 * i], sv[2 * i + 1]), off[i & 1]));
+            sv[2 * i] = v.x;
+            sv[2 * i + 1] = v.y;
+          }
+        };
         {
           tmem_ld_16x256b_x8(tS(g) + lane_addr, sv);
           tmem_wait_ld();
@@ -525,7 +557,7 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
               const uint64_t x = f32x2(sv[2 * i], sv[2 * i + 1]), u = mul_f32x2(x, x);
               const float2 uf = unpack_f32x2(u);
               um = fmax3(um, uf.x, uf.y);
-              const float2 v = unpack_f32x2(mul_f32x2(fma_f32x2(fma_f32x2(c2, u, c1), u, c0), x));
+              const float2 v = unpack_f32x2(fma_f32x2(fma_f32x2(fma_f32x2(c2, u, c1), u, c0), x, off[i & 1]));
               sv[2 * i] = v.x;
               sv[2 * i + 1] = v.y;
             }
@@ -546,7 +578,10 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
               tmem_wait_st();
               tmem_ld_16x256b_x8(tS(g) + lane_addr, sv);
               tmem_wait_ld();
+              take_off();
             }
+          } else {
+            take_off();
           }
           if (p.slopes) {
 #pragma unroll
@@ -554,9 +589,7 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
               const float d0 = static_cast<float>(kb - pos[hh]);  // of the first key from the query
               if (!p.prefix_lens) {
                 // Keys after the query are masked, so the distance of key
-                // 8 i + e is -(d0 + 8 i + e): the part common to the thread's
-                // scores goes into the softmax's reference.
-                shift[hh] = slope[hh] * d0;
+                // 8 i + e is -(d0 + 8 i + e); slope d0 is in `off`.
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -595,26 +628,26 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
               if ((bad >> (i >> 3)) & 1) sv[i] = -INFINITY;
           }
         }
-        // each row's maximum: the row's four threads (lanes 4 (t / 4) .. + 3)
+        // each row's maximum above its reference: the row's four threads (lanes
+        // 4 (t / 4) .. + 3)
         float mx[2];
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           float m = -INFINITY;
 #pragma unroll
           for (int i = 0; i < 8; ++i) m = fmax3(m, sv[4 * i + 2 * hh], sv[4 * i + 2 * hh + 1]);
-          m += shift[hh];
           m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
           mx[hh] = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
         }
-        // Move the reference up where a score passed it by more than kSlack; O
-        // and l follow, O once the last product into it is done. The
-        // tensor-memory loads and stores are warp-wide, so a warp rescales O when
-        // any of its rows moves, the other rows by exactly 1.
+        // Move the reference to a row's first maximum, and up where a score passed
+        // it by more than kSlack; O and l follow, once the last product into them
+        // is done. The tensor-memory loads and stores are warp-wide, so a warp
+        // rescales them when any of its rows moves, the other rows by exactly 1.
         bool moves[2], resc[2];
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          moves[hh] = mx[hh] > m_ref[hh] + kSlack;
-          resc[hh] = moves[hh] && j > 0 && m_ref[hh] != -INFINITY;
+          moves[hh] = set[hh] ? mx[hh] > kSlack : mx[hh] != -INFINITY;
+          resc[hh] = moves[hh] && set[hh];
         }
         if (__any_sync(kFull, moves[0] || moves[1])) {
           if (__any_sync(kFull, resc[0] || resc[1])) {
@@ -623,11 +656,11 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
             float alpha[2];
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              alpha[hh] = resc[hh] ? fast_exp2(m_ref[hh] - mx[hh]) : 1.f;
-              l_sum[hh] *= alpha[hh];
+              alpha[hh] = resc[hh] ? fast_exp2(-mx[hh]) : 1.f;
+              if constexpr (kPair) l_sum[hh] *= alpha[hh];
             }
 #pragma unroll 1
-            for (int c = 0; c < 64; c += 8) {  // 8 columns at a time: all 32 values at once would spill
+            for (int c = 0; c < (kPair ? 64 : 72); c += 8) {  // 8 columns at a time: all of them at once would spill
               float o[4];
               tmem_ld_16x256b_x1(tO + lane_addr + c, o);
               tmem_wait_ld();
@@ -638,43 +671,39 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
             tmem_wait_st();
           }
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh)
-            if (moves[hh]) m_ref[hh] = mx[hh];
-        }
-        // P = exp2(S - m_ref) as bf16 (and remainder) (16x128b: word 2 i + hh is
-        // column 4 i + q, the pair 8 i + 2 q, + 1 of row hh), with the row sums
-        uint32_t ph[16], pl[16];
-        uint64_t lp[2], mm[2];
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const float m_use = (m_ref[hh] == -INFINITY ? 0.f : m_ref[hh]) - shift[hh];  // all scores -inf: P = 0
-          mm[hh] = f32x2(m_use, m_use);
-          lp[hh] = f32x2(0.f, 0.f);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
-            const int w = 4 * i + 2 * hh;
-            const float2 d = unpack_f32x2(sub_f32x2(f32x2(sv[w], sv[w + 1]), mm[hh]));
-            const float p0 = fast_exp2(d.x), p1 = fast_exp2(d.y);
-            ph[2 * i + hh] = pack_bf16x2(p0, p1);
-            if constexpr (kPair) {
-              lp[hh] = add_f32x2(lp[hh], f32x2(p0, p1));
-              const float2 rem = bf16x2_remainder(ph[2 * i + hh], p0, p1);
-              pl[2 * i + hh] = pack_bf16x2(rem.x, rem.y);
-            } else {
-              const float2 r = bf16x2_to_float2(ph[2 * i + hh]);
-              lp[hh] = add_f32x2(lp[hh], f32x2(r.x, r.y));
+            if (moves[hh]) {
+              m_ref[hh] += mx[hh];
+              set[hh] = true;
             }
+            const float x = moves[hh] ? -mx[hh] : 0.f;
+            off[hh] = f32x2(x, x);
           }
+          take_off();
+        }
+        // P = exp2 of that, as bf16 (and remainder) (16x128b: word 2 i + hh is
+        // column 4 i + q, the pair 8 i + 2 q, + 1 of row hh)
+        uint32_t ph[16], pl[16];
+        [[maybe_unused]] uint64_t lp[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float p0 = fast_exp2(sv[2 * i]), p1 = fast_exp2(sv[2 * i + 1]);
+          ph[i] = pack_bf16x2(p0, p1);
+          if constexpr (kPair) {
+            lp[i & 1] = add_f32x2(lp[i & 1], f32x2(p0, p1));
+            const float2 rem = bf16x2_remainder(ph[i], p0, p1);
+            pl[i] = pack_bf16x2(rem.x, rem.y);
+          }
+        }
         tmem_st_16x128b_x8(tS(g) + lane_addr, ph);
         if constexpr (kPair) tmem_st_16x128b_x8(tS(g) + lane_addr + 32, pl);
         tmem_wait_st();
+        if constexpr (kPair) {
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const float2 a = unpack_f32x2(lp[hh]);
-          l_sum[hh] += a.x + a.y;
+          for (int hh = 0; hh < 2; ++hh) {
+            const float2 a = unpack_f32x2(lp[hh]);
+            l_sum[hh] += a.x + a.y;
+          }
         }
         // V rows that hold no key of the tile (outside its first and last key, or
         // of a page with a bad id) are zeroed once the stage's V copies have
@@ -704,19 +733,25 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
         load_rows(nt);
         store_q();
       }
-      // O / l for the live rows, l summed over the row's four threads. The
-      // decision is warp-uniform: the tensor-memory load is warp-wide.
+      // O / l for the live rows (with kPair l is summed over the row's four
+      // threads here). The decision is warp-uniform: the tensor-memory load is warp-wide.
       const bool done = !failed && mbar_wait_bounded(smem_addr(&pv_done[buf(g - 1)]), par(g - 1));
       if (__all_sync(kFull, done)) {
         tc_fence_after();
-        float o[32];
+        float o[32], sums[4];
         tmem_ld_16x256b_x8(tO + lane_addr, o);
+        if constexpr (!kPair) tmem_ld_16x256b_x1(tL + lane_addr, sums);
         tmem_wait_ld();
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          float l = l_sum[hh];
-          l += __shfl_xor_sync(kFull, l, 1);
-          l += __shfl_xor_sync(kFull, l, 2);
+          float l;
+          if constexpr (kPair) {
+            l = l_sum[hh];
+            l += __shfl_xor_sync(kFull, l, 1);
+            l += __shfl_xor_sync(kFull, l, 2);
+          } else {
+            l = sums[2 * hh];
+          }
           if (tok(hh) < t.n_ok) {
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const size_t at =
