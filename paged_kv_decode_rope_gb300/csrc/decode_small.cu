@@ -69,8 +69,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_small_kernel(const Sma
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g8 = lane >> 2, t4 = lane & 3;
   const size_t row0 = static_cast<size_t>(sg) * G;  // b hq + h G
-  grid_launch_dependents();
+  // the next kernel may start once every kernel before this one is complete
   grid_dependency_wait();
+  grid_launch_dependents();
   const int n = p.seq_lens[b];
   int lo = p.window > 0 ? max(n - p.window, 0) : 0;
   if (p.first_keys) lo = max(lo, p.first_keys[b]);

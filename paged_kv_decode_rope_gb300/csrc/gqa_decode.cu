@@ -660,8 +660,11 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
     for (int s = 0; s < C::kStages; ++s) mbar_init(bar0 + 8 * s, 1);
   fence_mbar_init();
   __syncthreads();
+  // (Scored mode lets the next kernel go only after its own wait: a step that
+  // follows may read, before its wait, what a kernel before this one wrote.)
+  if (kScored) grid_dependency_wait();
   grid_launch_dependents();
-  if (!kStep) grid_dependency_wait();
+  if (!kStep && !kScored) grid_dependency_wait();
   // The lengths, and with a plan in the workspace its header, its lengths,
   // its prefix sums and the bounds of this warp's first range, all loaded in
   // one round trip; the plan is taken only if it was made for this launch

@@ -298,8 +298,10 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
   __syncthreads();
   // The launch overlaps the end of the kernel before it, and the next one's
   // this one's end; logits, workspace and outputs are touched from here on.
-  grid_launch_dependents();
+  // The next kernel is let go only after the wait: what it reads before its
+  // own wait may come from a kernel before this one.
   grid_dependency_wait();
+  grid_launch_dependents();
   int chunk = 0;  // stages used so far
 
   if (warp == kLogWarps) {
