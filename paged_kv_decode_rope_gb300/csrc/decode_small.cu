@@ -23,6 +23,7 @@
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "score_cap.cuh"
 
 namespace pkv {
 namespace {
@@ -48,7 +49,7 @@ struct SmallParams {
   const float* slopes;        // [hq] or null
   int window;                 // 0: none
   float qscale;               // scores in base 2, or 2 log2(e) x when capped
-  float cap;                  // softcap * log2(e), 0: none
+  ScoreCap cap;
   int out_bf16;
   int* err;
 };
@@ -136,9 +137,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_small_kernel(const Sma
     }
     // head g8, tokens 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9
     float x[4] = {sc[0][0] + sc[0][2], sc[0][1] + sc[0][3], sc[1][0] + sc[1][2], sc[1][1] + sc[1][3]};
-    if (p.cap > 0.f) {  // cap tanh(x) = cap - 2 cap / (e^2x + 1); the scores are 2 log2(e) x
+    if (p.cap.cap > 0.f) {  // the scores are 2 log2(e) x
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = p.cap - 2.f * p.cap * fast_rcp(fast_exp2(x[i]) + 1.f);
+      for (int i = 0; i < 4; ++i) x[i] = capped_score(p.cap, x[i]);
     }
     bool seen[4];
     float mx = -INFINITY;
@@ -336,7 +337,7 @@ cudaError_t launch_decode_small(const DecodeLaunch& a, cudaStream_t stream) {
   p.slopes = a.slopes;
   p.window = a.window;
   p.qscale = static_cast<float>(a.softcap > 0.f ? 2.0 * a.scale / a.softcap * log2e : a.scale * log2e);
-  p.cap = static_cast<float>(a.softcap * log2e);
+  p.cap = make_score_cap(a.softcap);
   p.out_bf16 = a.out_bf16;
   p.err = a.err;
   const int segments = a.batch * a.num_kv_heads;

@@ -52,6 +52,7 @@
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "score_cap.cuh"
 
 namespace pkv {
 namespace {
@@ -152,7 +153,7 @@ struct DecodeParams {
   const int32_t* first_keys;  // [batch] or null
   const float* slopes;        // [hq] or null
   int window;                 // 0: none
-  float cap;                  // softcap * log2(e), 0: none (qscale then holds 2 log2(e) scale / softcap)
+  ScoreCap cap;               // (with a cap qscale holds 2 log2(e) scale / softcap)
   int out_bf16;
 };
 
@@ -1013,9 +1014,9 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
         const int seen = kScored ? __shfl_sync(kFull, cd_pos, t) : 0;
         const int lo = seen % kPage;  // slots before it are not visible
         if constexpr (kScored) {
-          if (p.cap > 0.f) {  // cap tanh(x) = cap - 2 cap / (e^2x + 1); the scores are 2 log2(e) x
+          if (p.cap.cap > 0.f) {  // the scores are 2 log2(e) x
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sv[k] = p.cap - 2.f * p.cap * fast_rcp(fast_exp2(sv[k]) + 1.f);
+            for (int k = 0; k < 4; ++k) sv[k] = capped_score(p.cap, sv[k]);
           }
           if (p.slopes) {
             const float dist = static_cast<float>(seen / kPage - 2 * tig);  // of this lane's first slot
@@ -1530,7 +1531,7 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream) {
       p.first_keys = a.first_keys ? a.first_keys + b0 : nullptr;
       p.slopes = a.slopes;
       p.window = a.window;
-      p.cap = static_cast<float>(static_cast<double>(a.softcap) * log2e);
+      p.cap = make_score_cap(a.softcap);
       if (a.softcap > 0.f) p.qscale = static_cast<float>(2.0 * static_cast<double>(a.scale) / a.softcap * log2e);
     }
     e = launch_group(group, *a.kv_map, p, grid, stream, mode);
