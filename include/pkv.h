@@ -518,7 +518,8 @@ typedef struct pkv_scoring {
  *   out          [batch][num_q_heads][64] of out_type (PKV_BF16: the fp32
  *                result rounded once), 16-byte aligned
  *   other arguments as for paged_gqa_decode (the automatic partition; the
- *   workspace is sized with pages_per_split = 0). max_blocks <= 2^23.
+ *   workspace is sized with pages_per_split = 0; little work may leave it
+ *   untouched). max_blocks <= 2^23.
  */
 int paged_gqa_decode_scored(const pkv_pool_t *pool, const float *q_rot, void *out, int out_type,
                             const int32_t *block_tables, int max_blocks, const int32_t *seq_lens,
@@ -532,7 +533,9 @@ int paged_gqa_decode_scored(const pkv_pool_t *pool, const float *q_rot, void *ou
  * sequence b's chunk is at position start_pos[b] + t; the sequence ends with
  * its chunk.
  *   q_rot        fp32 [total_tokens][num_q_heads][64], 16-byte aligned
- *   out          [total_tokens][num_q_heads][64] of out_type, 16-byte aligned
+ *   out          [total_tokens][num_q_heads][64] of out_type, 16-byte aligned.
+ *                With PKV_BF16 the softmax weights are rounded to bf16 as well
+ *                (and summed as rounded); with PKV_F32 they keep 16 bits.
  *   prefix_lens  int32 [batch] or NULL: keys below prefix_lens[b] are seen by
  *                queries before them too (a prefix that attends both ways)
  *   doc_starts   int32 [total_tokens] or NULL: first key position each chunk

@@ -5,8 +5,13 @@ its append into a shared BF16 page pool (``paged_kv_append_rope``), paged
 grouped-query decode attention with split-KV and a log-sum-exp merge
 (``paged_gqa_decode``), both fused into one step (``paged_decode_step``), and
 the standalone merge (``paged_kv_split_combine``), and the host page allocator
-with page-budget admission (``pkv_sched_*``, include/pkv_sched.h). This package
-is the thin Python binding with the same names; it only marshals arguments.
+with page-budget admission (``pkv_sched_*``, include/pkv_sched.h). A serving
+step of models with other positions or scores has calls of its own: block
+tables on the GPU (``paged_tables_build``), rotation and append by slot
+(``paged_rope_append``), attention with capped, biased or windowed scores
+(``paged_gqa_decode_scored``, ``paged_gqa_prefill_scored``) and
+log-probabilities (``token_logprobs``). This package is the thin Python binding
+with the same names; it only marshals arguments.
 """
 from ._binding import (  # noqa: F401
     ERR_NO_PAGES,

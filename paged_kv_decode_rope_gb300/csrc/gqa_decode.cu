@@ -47,6 +47,12 @@
 //    merges them, the others publish and go on. A CTA only waits for CTAs of
 //    earlier groups, and no second kernel (with its launch and dependency
 //    hand-off) is needed.
+//  * Scored mode (paged_gqa_decode_scored) caps, biases and limits the scores
+//    between the two products and starts every sequence at the page of its
+//    first visible key: 256 sequences of up to 8192 tokens, window 4096, cap,
+//    32 + 8 heads 228 us (6.50 TB/s of K and V, 96% of the copy bandwidth); 32
+//    of 1000 to 32768 tokens, distance bias, 14 + 2 heads 52.3 us (5.56 TB/s).
+//    Little work goes to decode_small.cu.
 #include <atomic>
 #include <cmath>
 
@@ -1194,10 +1200,12 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
         for (uint32_t look = 0; look < p.merge_looks && !done; ++look) {
           // Two or more other groups: stage them, so that their round trips
           // overlap (not in a warp that timed out: page copies may still land
-          // in its ring). Only groups of 5-8 heads: their few KV heads make
-          // segments long enough to span three or more CTAs, and their kernel
-          // has the registers to spare; in the register-capped kernel of 1-4
-          // heads the extra code cost 0.2 us per layer where it never ran.
+          // in its ring). Without scoring, only groups of 5-8 heads: their few
+          // KV heads make segments long enough to span three or more CTAs, and
+          // their kernel has the registers to spare; in the register-capped
+          // kernel of 1-4 heads the extra code cost 0.2 us per layer where it
+          // never ran. Scored mode has groups of 1-4 heads do it as well: one
+          // sequence of 30000 tokens 28.7 -> 23.6 us.
           if constexpr (G > 4 || kScored) {
             if (g_last - g_first >= 2 && !failed) {
               done = gather_groups_staged<G>(all, pc, p.slots, ring0, grp, g_first, g_last, g8,

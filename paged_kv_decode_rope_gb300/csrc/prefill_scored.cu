@@ -20,16 +20,20 @@
 // everywhere in this library, and so does P where the output is fp32 (kPair).
 // Where the output is bf16, P is rounded to bf16 once, and the tensor core sums
 // the rounded P, so that the weights still sum to one (and no instruction of the
-// softmax is spent on the sums); what is left (1.1 to 1.35
-// times the error of rounding the output alone, over 16 to 2048 keys) costs a
-// quarter less of the softmax's arithmetic and half the P V products. Scores,
-// sums and O are fp32. The
-// reference maximum of a row moves only when a score passes it by more than
+// softmax is spent on the sums); what is left (1.1 to 1.35 times the error of
+// rounding the output alone, over 16 to 2048 keys) costs a quarter less of the
+// softmax's arithmetic and half the P V products. Scores, sums and O are fp32.
+// The reference maximum of a row moves only when a score passes it by more than
 // kSlack (base 2), so P <= 2^kSlack.
 //
-// What bounds it: the softmax warps' arithmetic (about 1700 cycles a step with
-// two CTAs on an SM, 2400 with a cap), and around it the latencies of a tile's
-// start and end. With a CTA a tile these took 13,000 of the 20,000 cycles of a
+// Measured, 4 chunks of 2048 tokens, 32 + 8 heads, window 1024 (51.6 GFLOP):
+// 130 us with a cap (397 TFLOP/s), 115 without, 141 with a distance bias, 150
+// with a cap and fp32 out, 195 with a cap whose scores pass kPolyMax.
+//
+// What bounds it: the softmax warps' arithmetic (a step of 128 x 64 scores
+// takes an SM some 1450 cycles with a cap and 1280 without; its exp2s alone are
+// 512 of them), and around it the latencies of a tile's start and end. With
+// a CTA a tile these took 13,000 of the 20,000 cycles of a
 // tile of three steps (window 128): launch, tensor memory, tile, query rows,
 // first keys, last product, epilogue, one after the other. So CTAs stay, two on
 // an SM, and everything but the softmax runs ahead into the next tile: the key
@@ -178,10 +182,10 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
   // Step j of a tile takes the 64 keys of block key_block(j). With a distance
   // bias the last block comes first: the largest scores are there, and the
   // reference maximum found in the first step stands (from the first block on
-  // it moved in nearly every step: 280 us instead of 177 for 4 x 2048 tokens).
+  // it moved in nearly every step: 1.6 times the time for 4 x 2048 tokens).
   // Without one the first block comes first, a full one where the last one
   // holds few keys of the early rows, so that their first maximum is soon
-  // passed (181 us against 205 with a window of 1024). Page ids come in windows
+  // passed (0.88 of the time with a window of 1024). Page ids come in windows
   // of 32, eight steps: lane i of window m holds page window_page(m) + i, and
   // step j's four pages are lanes window_lane(j) .. + 3.
   const bool down = p.slopes != nullptr;
