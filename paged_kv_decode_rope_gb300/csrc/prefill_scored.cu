@@ -30,9 +30,10 @@
 // 130 us with a cap (397 TFLOP/s), 115 without, 141 with a distance bias, 150
 // with a cap and fp32 out, 195 with a cap whose scores pass kPolyMax.
 //
-// What bounds it: the softmax warps' arithmetic (a step of 128 x 64 scores
-// takes an SM some 1450 cycles with a cap and 1280 without; its exp2s alone are
-// 512 of them), and around it the latencies of a tile's start and end. With
+// What bounds it: the softmax warps' instructions (a step of 128 x 64 scores
+// takes an SM some 1450 cycles with a cap and 1280 without, about 420
+// instructions a warp; 62% of the cycles issue one, the special-function pipe is
+// 18% busy), and around it those of a tile's start and end, some 3700 cycles. With
 // a CTA a tile these took 13,000 of the 20,000 cycles of a
 // tile of three steps (window 128): launch, tensor memory, tile, query rows,
 // first keys, last product, epilogue, one after the other. So CTAs stay, two on
