@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_small_kernel(const Sma
   __syncthreads();
   // element i of the segment's G rows: head g = i / 64, dim i % 64
   auto finish = [&](int i, float sum, float total) {
-    const float y = total > 0.f ? sum / total : 0.f;
+    const float y = total == 0.f ? 0.f : sum / total;  // (a NaN score makes the row NaN)
     if (p.out_bf16) {
       static_cast<uint16_t*>(p.out)[row0 * kHeadDim + i] = static_cast<uint16_t>(pack_bf16x2(y, 0.f));
     } else {
@@ -237,13 +237,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_small_kernel(const Sma
     float mx = -INFINITY, sum = 0.f, total = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][g]);
-    if (mx != -INFINITY) {
+    const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = fast_exp2(s_m[w][g] - mx);
-        sum += f * s_acc[w][g][d];
-        total += f * s_l[w][g];
-      }
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = fast_exp2(s_m[w][g] - ref);
+      sum += f * s_acc[w][g][d];
+      total += f * s_l[w][g];
     }
     if (alone) {
       finish(i, sum, total);
@@ -275,13 +274,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_small_kernel(const Sma
     float mx = -INFINITY, sum = 0.f, total = 0.f;
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) mx = fmaxf(mx, cm[r]);
-    if (mx != -INFINITY) {
+    const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) {
-        const float f = fast_exp2(cm[r] - mx);
-        sum += f * ca[r];
-        total += f * cl[r];
-      }
+    for (int r = 0; r < kMaxCluster; ++r) {
+      const float f = fast_exp2(cm[r] - ref);
+      sum += f * ca[r];
+      total += f * cl[r];
     }
     finish(i, sum, total);
   }

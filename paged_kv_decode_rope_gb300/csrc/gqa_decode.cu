@@ -1119,7 +1119,8 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
         for (int d = 0; d < 8; ++d) of[d] = make_float2(o[d][0] + o[d][2], o[d][1] + o[d][3]);
         float lsum = l_run + __shfl_xor_sync(kFull, l_run, 1);
         lsum += __shfl_xor_sync(kFull, lsum, 2);
-        const float mh = m_run;
+        // (scored: a piece of nothing but NaN scores has no maximum; with one it is merged, not skipped)
+        const float mh = kScored && isnan(lsum) ? 0.f : m_run;
         const bool live = g8 < G;
         const int bh = __shfl_sync(kFull, cd_bh, t);
         const int b = bh / p.hkv, h = bh - b * p.hkv;
@@ -1252,7 +1253,7 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, 1)
         for (int d = 0; d < 8; ++d) pc.acc[d] = make_float2(o[d][0] + o[d][2], o[d][1] + o[d][3]);
         pc.l = l_run + __shfl_xor_sync(kFull, l_run, 1);
         pc.l += __shfl_xor_sync(kFull, pc.l, 2);
-        pc.m = m_run;
+        pc.m = kScored && isnan(pc.l) ? 0.f : m_run;
         merge_segment(head.x, pc, warp, head.y, head.z);
       }
       __syncthreads();  // the slots are free for the next group
