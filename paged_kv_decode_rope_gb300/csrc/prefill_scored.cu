@@ -26,9 +26,10 @@
 // The reference maximum of a row moves only when a score passes it by more than
 // kSlack (base 2), so P <= 2^kSlack.
 //
-// Measured, 4 chunks of 2048 tokens, 32 + 8 heads, window 1024 (51.6 GFLOP):
-// 130 us with a cap (397 TFLOP/s), 115 without, 141 with a distance bias, 150
-// with a cap and fp32 out, 195 with a cap whose scores pass kPolyMax.
+// Measured, 4 chunks of 2048 tokens, 32 + 8 heads: with a window of 1024 (51.6
+// GFLOP) 132 us with a cap (391 TFLOP/s), 115 without, 214 with a cap whose
+// scores pass kPolyMax; over all keys 133 us, 155 with a cap, 141 with a
+// distance bias, 150 with fp32 out.
 //
 // What bounds it: the softmax warps' instructions (a step of 128 x 64 scores
 // takes an SM some 1450 cycles with a cap and 1280 without, about 420
@@ -568,22 +569,29 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
             }
             constexpr double kMostT = 2.0 * 1.4426950408889634 * kPolyMax;
             if (__any_sync(kFull, !(um <= static_cast<float>(kMostT * kMostT)))) {
-              // The exact cap, in place in tensor memory, 8 columns at a time (with
-              // both forms over all 32 scores of a thread in one path its
-              // registers spilled, and every step took 1.5 times as long).
+              // The exact cap where it is due, in place in tensor memory, 8 columns
+              // at a time (with both forms over all 32 scores of a thread in one
+              // path its registers spilled, and every step took 1.5 times as
+              // long). A score keeps the form and the roundings that it has above:
+              // rows of keys that are not the tile's hold anything, and what they
+              // score must not show in the others.
 #pragma unroll 1
               for (int c = 0; c < 64; c += 8) {
                 float x[4];
                 tmem_ld_16x256b_x1(tS(g) + lane_addr + c, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = fmaf(-2.f * p.cap, fast_rcp(fast_exp2(x[i]) + 1.f), p.cap);
+                for (int i = 0; i < 4; ++i) {
+                  const float u = x[i] * x[i], o = unpack_f32x2(off[i >> 1]).x;
+                  const float near = fmaf(fmaf(fmaf(p.poly[2], u, p.poly[1]), u, p.poly[0]), x[i], o);
+                  const float far = fmaf(-2.f * p.cap, fast_rcp(fast_exp2(x[i]) + 1.f), p.cap) + o;
+                  x[i] = u <= static_cast<float>(kMostT * kMostT) ? near : far;
+                }
                 tmem_st_16x256b_x1(tS(g) + lane_addr + c, x);
               }
               tmem_wait_st();
               tmem_ld_16x256b_x8(tS(g) + lane_addr, sv);
               tmem_wait_ld();
-              take_off();
             }
           } else {
             take_off();

@@ -67,3 +67,33 @@ def test_prefill(softcap):
                                      ws, softcap=cap)
     agree(*out, q, pool)
     handle.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("softcap", [20.0, 1e6])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_prefill_does_not_depend_on_what_was_there(softcap, dtype):
+    """Bit for bit the same after a call that left large keys in the memory of the SMs and after one that left zeros."""
+    lens = [1, 40, 333, 5, 18]
+    pool, tables, g = setup(lens, 24)
+    q = (torch.randn(sum(lens), HQ, 64, generator=g) * 0.05).cuda()
+    ws = pkv.alloc_prefill_workspace(4096, 12, 24)
+
+    def run(pool, tables, q, chunks, out):
+        handle = pkv.kv_pool_create(pool, HKV)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        cu = torch.tensor([0] + [sum(chunks[:i + 1]) for i in range(len(chunks))], **i32)
+        pkv.paged_gqa_prefill_scored(handle, q, out, tables, cu, torch.zeros(len(chunks), **i32), SCALE, ws,
+                                     softcap=softcap)
+        torch.cuda.synchronize()
+        handle.close()
+        return out
+
+    outs = []
+    for value in (2.0 ** 14, 0.0):
+        other = torch.full((24 * 12, HKV, 2, 16, 64), value, dtype=torch.bfloat16, device="cuda")
+        t = torch.arange(24 * 12, dtype=torch.int32, device="cuda").view(12, 24)[:, :21].contiguous()
+        run(other, t, torch.ones(12 * 330, HQ, 64, device="cuda"), [330] * 12,
+            torch.empty(12 * 330, HQ, 64, dtype=dtype, device="cuda"))
+        outs.append(run(pool, tables, q, lens, torch.empty(sum(lens), HQ, 64, dtype=dtype, device="cuda")))
+    assert torch.equal(*outs)
