@@ -116,6 +116,11 @@ int integer(PyObject* o, const char* name) {
   if (v > INT32_MAX || v < INT32_MIN) refuse(PyExc_ValueError, std::string(name) + " is too large");
   return static_cast<int>(v);
 }
+int truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused();
+  return v;
+}
 float real(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw Refused();
@@ -200,7 +205,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                       ints<const int32_t>(a[6], {tokens}, "slot_map"), ints<const int32_t>(a[7], {tokens}, "positions"),
                       size_of(tokens, "tokens"), size_of(hq, "heads"), pointer(table, at::kByte, "rope_table"),
                       size_of(table.size(0) / static_cast<int64_t>(PKV_ROPE_TABLE_BYTES(1)), "rope_table"),
-                      integer(a[9], "rot_dim"), PyObject_IsTrue(a[10]) == 1, stream_of(a[11], q, "q"));
+                      integer(a[9], "rot_dim"), truth(a[10]), stream_of(a[11], q, "q"));
   });
 }
 
