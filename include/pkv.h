@@ -548,8 +548,8 @@ int paged_gqa_decode_scored(const pkv_pool_t *pool, const float *q_rot, void *ou
  * Pages before the first key that a tile of rows sees (of at most 128 / group
  * tokens) are neither read nor looked up.
  * A value that is not finite can reach the rows of neighbouring tokens of its
- * sequence (of one tile) that do not see it; slots outside every row's keys
- * may hold anything. Two launches.
+ * sequence (of one tile) that do not see it; slots before the first key that a
+ * tile's rows see, and past the last one, may hold anything. Two launches.
  */
 int paged_gqa_prefill_scored(const pkv_pool_t *pool, const float *q_rot, void *out, int out_type,
                              const int32_t *block_tables, int max_blocks, const int32_t *cu_tokens,

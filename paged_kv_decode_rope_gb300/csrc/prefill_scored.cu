@@ -254,11 +254,15 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
           t.end = static_cast<int>(min(static_cast<long long>(max(prefix, 0)),
                                        min(static_cast<long long>(start) + (c1 - c0), p.pos_cap)));
           if (t.n_ok < tile.z && lane == 0) atomicOr(p.err, PKV_ERR_SEQ_LEN);
-          // the least first key of the tokens that see one
-          int lo = INT_MAX;
+          // the least first key and the last key of the tokens that see one
+          int lo = INT_MAX, hi = -1;
           for (int i = lane; i < t.n_ok; i += 32) {
             const int l = first_key(t.row0 + i, tile.w + i);
-            if (l <= max(tile.w + i, t.end - 1)) lo = min(lo, l);
+            const int last = max(tile.w + i, t.end - 1);
+            if (l <= last) {
+              lo = min(lo, l);
+              hi = max(hi, last);
+            }
             // its query rows, to L2
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
                              p.q_rot + (static_cast<size_t>(t.row0 + i) * p.hq + t.h * G) * kHeadDim),
@@ -266,6 +270,7 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
                          : "memory");
           }
           lo = __reduce_min_sync(kFull, lo);
+          hi = __reduce_max_sync(kFull, hi);
           if (lo == INT_MAX) t.n_ok = 0;  // no row sees a key
           // rows past n_ok, all of them when no row sees a key
           const int words = G * kHeadDim / (kPair ? 1 : 2);
@@ -278,7 +283,7 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
           t.lo = lo - t.key0;
           t.pos0 = tile.w - t.key0;
           t.end -= t.key0;
-          t.last = max(t.pos0 + t.n_ok, t.end) - 1;
+          t.last = hi - t.key0;
           t.n_pages = t.last / kPage + 1;
           t.n_steps = (t.n_pages + 3) / 4;
           break;

@@ -418,3 +418,12 @@ def test_library_refusals():
             args[i] = bad
             assert lib.paged_gqa_prefill_scored(*args) == -22, (i, bad)
     handle.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("chunks,starts", [([16, 0], [0, 0]), ([0, 16], [0, 270]), ([132, 1, 1], [1, 0, 1])])
+def test_prefill_keys_past_the_last_one_seen_may_hold_anything(chunks, starts, dtype):
+    # every third token sees nothing, the last of some tiles among them: its own key is NaN
+    run_prefill(47, 8, 4, chunks, starts, softcap=20.0, docs=lambda b, p: p // 5 * 5 + (1000 if p % 3 == 0 else 0),
+                dtype=dtype)
