@@ -5,8 +5,8 @@
 // some 2000 instructions once (lengths, prefix sums, partition, TMA ring, merges
 // in shared memory, then through the workspace), one latency after the other:
 // 12 us for eight sequences of up to 2048 tokens and 32 + 8 heads, 6 us for
-// sequences of one token. Here a segment is a cluster of 1 to 8 CTAs, as many as
-// keep all CTAs on the GPU at once; its warps take its pages in turn, and their
+// sequences of one token. Here a segment is a cluster of 1 to 16 CTAs, as many as
+// keep all clusters on the GPU at once; its warps take its pages in turn, and their
 // pieces meet in shared memory, then across the cluster through distributed
 // shared memory: no partition, no workspace, no spinning. A segment that one
 // CTA's warps cover is done by its first CTA alone.
@@ -19,6 +19,8 @@
 // and 2 t + 9, and column n of product d is dim 8 n + d. Q (rows 0-7: heads) and
 // P enter as bf16 with their remainders in rows 8-15, as in gqa_decode.cu. The
 // next page's loads are in flight while a page is worked on.
+#include <atomic>
+
 #include <cooperative_groups.h>
 
 #include "pkv_device.cuh"
@@ -32,7 +34,12 @@ namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
+// Segments of up to this many pages take clusters of at most 8 CTAs: one
+// sequence of 1024 tokens (64 pages) 4.8 us against 5.2 with 16, of 2048 6.0
+// against 5.7, of 8192 12.0 against 9.3 (32 + 8 heads; with 14 + 2 5.0 / 4.9, 6.2 /
+// 5.2, 12.1 / 8.3, but eight sequences of 2048 7.2 / 7.5).
+constexpr int kShortPages = 160;
 constexpr int kCtas = 3;  // CTAs a SM
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -286,8 +293,44 @@ __global__ void __launch_bounds__(kThreads, kCtas) decode_small_kernel(const Sma
   cluster.sync();  // no CTA leaves while another reads its piece
 }
 
+// Clusters of `ctas` CTAs that run at once. (SMs come in groups of which a
+// cluster takes one, so this is less than the CTAs that fit over `ctas`: 64
+// clusters of 7 do not fit beside one another although their CTAs would, and
+// take 13 us where 64 of 4 take 10.)
 template <int G>
-cudaError_t launch(const SmallParams& p, int segments, int ctas, cudaStream_t stream) {
+int clusters_at_once(int device, int ctas) {
+  static std::atomic<int> cache[64][kMaxCluster + 1];  // found + 1
+  std::atomic<int>& known = cache[device & 63][ctas];
+  int n = known.load(std::memory_order_relaxed) - 1;
+  if (n >= 0) return n;
+  if (ctas > 8) {  // more than every GPU has to grant
+    const cudaError_t e =
+        cudaFuncSetAttribute(decode_small_kernel<G>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return -1;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, decode_small_kernel<G>, &cfg) != cudaSuccess) return -1;
+  known.store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+template <int G>
+cudaError_t launch(const SmallParams& p, int segments, int most_ctas, int device, cudaStream_t stream) {
+  // the most CTAs a segment with which all segments run at once
+  int ctas = most_ctas;
+  for (; ctas > 1; --ctas) {
+    const int most = clusters_at_once<G>(device, ctas);
+    if (most < 0) return cudaGetLastError();
+    if (segments <= most) break;
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -307,16 +350,18 @@ cudaError_t launch(const SmallParams& p, int segments, int ctas, cudaStream_t st
 
 // Little work, as far as the host can tell: the pages that the block tables (or
 // the window) can hold, over all segments, and of one segment. Measured against
-// the general kernel (lengths between half and all of what the tables hold, 32 +
-// 8 heads): 3.4 against 6.2 us for 8 sequences of one token, 9.6 / 12.6 for 8
-// of 2048 (8192 pages in all), 14.2 / 15.8 for 16 of 2048 and 13.1 / 15.6 for 32 of
-// 1024 (16384), but 26.1 / 21.5 for 32 of 2048 (32768), where an even partition of
-// all pages counts. One sequence (14 + 2 heads): 11.5 / 23.4 us at 512 pages; about
-// 0.5 us more for every further page of a warp, so at 2000 pages it is behind.
-constexpr long long kMostPages = 20480, kMostSegmentPages = 1024;
+// the general kernel (lengths between half and all of what the tables hold), 32 +
+// 8 heads: 3.9 against 6.2 us for 8 sequences of one token, 9.3 / 12.6 for 8 of
+// 2048 (8192 pages in all), 12.3 / 15.8 for 16 of 2048 and 13.4 / 15.6 for 32 of
+// 1024 (16384), but 26.2 / 21.8 for 32 of 2048 (32768), where an even partition of
+// all pages counts. 14 + 2 heads, 2048 pages a segment: 20.0 / 53.5 for one
+// sequence, 21.8 / 28.2 for four; 4096 pages: 35.4 / 43.9 and 48.9 / 37.0.
+constexpr long long kMostPages = 20480, kMostSegmentPages = 2048;
+static int segment_pages(const DecodeLaunch& a) {
+  return a.window > 0 && a.window / kPage + 2 < a.max_blocks ? a.window / kPage + 2 : a.max_blocks;
+}
 bool decode_small_fits(const DecodeLaunch& a) {
-  long long pages = a.max_blocks;
-  if (a.window > 0 && a.window / kPage + 2 < pages) pages = a.window / kPage + 2;
+  const long long pages = segment_pages(a);
   return pages <= kMostSegmentPages && pages * a.batch * a.num_kv_heads <= kMostPages;
 }
 
@@ -342,18 +387,16 @@ cudaError_t launch_decode_small(const DecodeLaunch& a, cudaStream_t stream) {
   int device = 0;
   const cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
-  // as many CTAs a segment as run at once
-  int ctas = kMaxCluster;
-  while (ctas > 1 && segments * ctas > kCtas * device_sm_count(device)) ctas /= 2;
+  const int most_ctas = segment_pages(a) > kShortPages ? kMaxCluster : 8;
   switch (a.num_q_heads / a.num_kv_heads) {
-    case 1: return launch<1>(p, segments, ctas, stream);
-    case 2: return launch<2>(p, segments, ctas, stream);
-    case 3: return launch<3>(p, segments, ctas, stream);
-    case 4: return launch<4>(p, segments, ctas, stream);
-    case 5: return launch<5>(p, segments, ctas, stream);
-    case 6: return launch<6>(p, segments, ctas, stream);
-    case 7: return launch<7>(p, segments, ctas, stream);
-    case 8: return launch<8>(p, segments, ctas, stream);
+    case 1: return launch<1>(p, segments, most_ctas, device, stream);
+    case 2: return launch<2>(p, segments, most_ctas, device, stream);
+    case 3: return launch<3>(p, segments, most_ctas, device, stream);
+    case 4: return launch<4>(p, segments, most_ctas, device, stream);
+    case 5: return launch<5>(p, segments, most_ctas, device, stream);
+    case 6: return launch<6>(p, segments, most_ctas, device, stream);
+    case 7: return launch<7>(p, segments, most_ctas, device, stream);
+    case 8: return launch<8>(p, segments, most_ctas, device, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -122,9 +122,9 @@ def run_decode(seed, hq, hkv, lens, softcap=0.0, alibi=False, window=0, first=No
 
 LENS = [1, 2, 15, 16, 17, 33, 160, 700]
 
-# Block tables that could hold long sequences (1100 pages) take the general
+# Block tables that could hold long sequences (2100 pages) take the general
 # kernel, narrow ones the kernel for little work.
-WIDE = pytest.mark.parametrize("max_blocks", [None, 1100], ids=["narrow", "wide"])
+WIDE = pytest.mark.parametrize("max_blocks", [None, 2100], ids=["narrow", "wide"])
 
 
 @pytest.mark.gpu
@@ -187,7 +187,7 @@ def test_decode_without_scoring_is_the_plain_decode():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("max_blocks", [4, 1100], ids=["narrow", "wide"])
+@pytest.mark.parametrize("max_blocks", [4, 2100], ids=["narrow", "wide"])
 def test_decode_bad_lengths_and_pages(max_blocks):
     rng = np.random.default_rng(8)
     lens = [40, 0, -3, 16 * max_blocks + 1, 20]
@@ -427,3 +427,12 @@ def test_prefill_keys_past_the_last_one_seen_may_hold_anything(chunks, starts, d
     # every third token sees nothing, the last of some tiles among them: its own key is NaN
     run_prefill(47, 8, 4, chunks, starts, softcap=20.0, docs=lambda b, p: p // 5 * 5 + (1000 if p % 3 == 0 else 0),
                 dtype=dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_decode_of_many_windowed_sequences(dtype):
+    # enough pages for the general kernel although each sequence sees at most three (and two launches)
+    lens = [1 + (7 * i) % 90 for i in range(1100)]
+    run_decode(61, 16, 8, lens, 30.0, True, 30, first=[max(0, n - 1 - (5 * i) % 50) for i, n in enumerate(lens)],
+               dtype=dtype)

@@ -23,7 +23,7 @@ def setup(max_blocks, seq, pos):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("softcap", [0.0, 30.0])
-@pytest.mark.parametrize("max_blocks", [48, 1100])  # either decode kernel
+@pytest.mark.parametrize("max_blocks", [48, 2100])  # either decode kernel
 @pytest.mark.parametrize("seq,pos", [(1, [5]), (1, [699]), (1, range(700)), (0, range(16)), (2, [0]), (3, [332])])
 def test_decode(seq, pos, max_blocks, softcap):
     pool, tables, g = setup(max_blocks, seq, pos)
