@@ -561,7 +561,8 @@ int paged_gqa_prefill_scored(const pkv_pool_t *pool, const float *q_rot, void *o
 /* Largest number of alternatives token_logprobs gives. */
 #define PKV_MAX_TOP 32
 
-/* Device bytes of workspace token_logprobs needs (0 for invalid sizes). */
+/* Device bytes of workspace token_logprobs needs (0 for invalid sizes): the
+ * same for all sizes, so that one workspace serves calls of any. */
 size_t token_logprobs_workspace_bytes(int rows, int vocab, int top);
 
 /*

@@ -573,8 +573,8 @@ def token_logprobs_workspace_bytes(rows: int, vocab: int, top: int) -> int:
 
 
 def alloc_logprobs_workspace(rows: int, vocab: int, top: int, device=None) -> torch.Tensor:
-    """A zero-filled workspace for token_logprobs on up to `rows` rows (each
-    call leaves it ready for the next)."""
+    """A zero-filled workspace for token_logprobs (each call leaves it ready
+    for the next, of any size)."""
     n = token_logprobs_workspace_bytes(rows, vocab, top)
     if n == 0:
         raise ValueError("invalid logprobs sizes")

@@ -670,7 +670,19 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
   }
 }
 
-size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+// The workspace: counter and tickets, then the split pieces' sums and keys. Its
+// places depend on the GPU alone (fewer rows are split than CTAs run at once, into
+// no more pieces than that), not on a call's sizes, so a call finds its
+// counter and tickets where every other call left them at zero.
+struct Workspace {
+  size_t sums, keys, bytes;  // offsets; tickets follow the counter at 0
+  explicit Workspace(int ctas) {
+    auto align256 = [](size_t n) { return (n + 255) / 256 * 256; };
+    sums = align256(sizeof(int) * (static_cast<size_t>(ctas) + 1));
+    keys = sums + align256(sizeof(float4) * ctas);
+    bytes = keys + sizeof(uint64_t) * kTop * ctas;
+  }
+};
 
 // How the rows are cut for `ctas` CTAs: whole rounds of a row a CTA first; the
 // rows left over (or all, when they are fewer) are split over as many CTAs as
@@ -697,14 +709,10 @@ extern "C" {
 size_t token_logprobs_workspace_bytes(int rows, int vocab, int top) {
   using namespace pkv;
   if (rows < 1 || vocab < 1 || top < 0 || top > PKV_MAX_TOP || top > vocab) return 0;
-  // the counter, a ticket a row, and room for as many split pieces as CTAs run at once
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return 0;
   const int sms = device_sm_count(device);
-  if (sms < 1) return 0;
-  const size_t pieces = static_cast<size_t>(kLogCtas) * sms;
-  return align256(sizeof(int) * (static_cast<size_t>(rows) + 1)) + align256(sizeof(float4) * pieces) +
-         sizeof(uint64_t) * kTop * pieces;
+  return sms < 1 ? 0 : Workspace(kLogCtas * sms).bytes;
 }
 
 int token_logprobs(const void* logits, int logits_type, long long row_stride, int rows, int vocab,
@@ -754,10 +762,9 @@ int token_logprobs(const void* logits, int logits_type, long long row_stride, in
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.counter = reinterpret_cast<int*>(ws);
   p.tickets = p.counter + 1;
-  ws += align256(sizeof(int) * (static_cast<size_t>(rows) + 1));
-  p.sums = reinterpret_cast<float4*>(ws);
-  ws += align256(sizeof(float4) * static_cast<size_t>(ctas));
-  p.keys = reinterpret_cast<uint64_t*>(ws);
+  const Workspace at(ctas);
+  p.sums = reinterpret_cast<float4*>(ws + at.sums);
+  p.keys = reinterpret_cast<uint64_t*>(ws + at.keys);
   auto kernel = logits_type == PKV_BF16 ? logprobs_kernel<uint16_t> : logprobs_kernel<float>;
   constexpr int kSmem = kLogStages * kStageVectors * 16;
   static std::atomic<bool> ready[2];
