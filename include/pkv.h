@@ -419,8 +419,7 @@ int paged_kv_split_combine(const float *o_part, const float *lse_part, const int
  *   free_pages   int32 [num_free]: ids of free pages, used from entry
  *                *free_head on
  *   free_head    int32 [1], 0 <= *free_head <= num_free;  free_head_out int32
- *                [1] out: the next unused entry. They must not be the same
- *                word: pass the one step's output as the next one's input.
+ *                [1] out: the next unused entry.
  *   block_tables int32 [num_layers][batch][max_blocks], in and out: the new
  *                blocks' entries are written, the others kept
  *   cu_tokens    int32 [batch+1] out: first token of each sequence, the last
@@ -432,6 +431,11 @@ int paged_kv_split_combine(const float *o_part, const float *lse_part, const int
  *                out: position 0 and slot -1 for entries past the step's
  *                tokens and for tokens of a sequence that is not served.
  *                capacity < 2^29.
+ * No array that is written (free_head_out, block_tables, cu_tokens, seq_lens,
+ * positions, slot_map) may overlap another one of the call (-EINVAL): lengths
+ * and head are read by the whole grid while the new ones are written, so pass
+ * one step's seq_lens and free_head_out as the next one's inputs instead of
+ * updating them in place.
  * A sequence is not served, and takes no pages, when a length is negative,
  * start + new passes max_blocks*16 or its tokens end past capacity
  * (PKV_ERR_SEQ_LEN), or when it needs pages and the list does not hold those

@@ -494,9 +494,10 @@ def paged_tables_build(pool: KVPool, start_pos: torch.Tensor, new_tokens: torch.
                        positions: torch.Tensor, slot_map: torch.Tensor, stream=None) -> None:
     """A step's block tables, slot maps and positions from its lengths.
     start_pos/new_tokens [B], free_pages [F], free_head [1] int32;
-    block_tables [L,B,max_blocks] int32 in and out; free_head_out [1] (not
-    free_head itself), cu_tokens [B+1], seq_lens [B], positions [T],
-    slot_map [L,T] int32 out, T the capacity in tokens."""
+    block_tables [L,B,max_blocks] int32 in and out; free_head_out [1],
+    cu_tokens [B+1], seq_lens [B], positions [T], slot_map [L,T] int32 out, T
+    the capacity in tokens. What is written must overlap nothing else: a step's
+    seq_lens and free_head_out are the next one's start_pos and free_head."""
     rc = (_call_module or _native()).paged_tables_build(
         pool._handle or 0, start_pos, new_tokens, free_pages, free_head, free_head_out, block_tables, cu_tokens,
         seq_lens, positions, slot_map, stream)
