@@ -29,6 +29,9 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL: the legacy default
  *    stream). Every call only enqueues work on it; nothing synchronises except
  *    pkv_get_error.
+ *  - A call runs on the current device, which must be the one that was current
+ *    when the pool was created. The calls that take pkv_scoring,
+ *    paged_tables_build and paged_rope_append return -EINVAL where it is not.
  *  - Checks that need device data (lengths, page ids) are made by the
  *    kernels. A failed check skips the affected sequence or page and sets a
  *    bit (PKV_ERR_*) in the pool's error word; no kernel traps.

@@ -513,9 +513,10 @@ def paged_rope_table_build_freqs(inv_freq, num_positions: int, table: torch.Tens
     inv_freq = [float(f) for f in inv_freq]
     if table.numel() < num_positions * ROPE_TABLE_BYTES_PER_ROW:
         raise ValueError("rope table too small")
-    rc = lib().paged_rope_table_build_freqs((_d * len(inv_freq))(*inv_freq), len(inv_freq), float(magnitude),
-                                            int(num_positions), _dev(table, torch.uint8, "table", 1),
-                                            _stream(stream))
+    at = _dev(table, torch.uint8, "table", 1)
+    with torch.cuda.device(table.device):
+        rc = lib().paged_rope_table_build_freqs((_d * len(inv_freq))(*inv_freq), len(inv_freq), float(magnitude),
+                                                int(num_positions), at, _stream(stream))
     _check("paged_rope_table_build_freqs", rc)
 
 
@@ -576,10 +577,11 @@ def token_logprobs_workspace_bytes(rows: int, vocab: int, top: int) -> int:
 def alloc_logprobs_workspace(rows: int, vocab: int, top: int, device=None) -> torch.Tensor:
     """A zero-filled workspace for token_logprobs (each call leaves it ready
     for the next, of any size)."""
-    n = token_logprobs_workspace_bytes(rows, vocab, top)
-    if n == 0:
-        raise ValueError("invalid logprobs sizes")
-    return torch.zeros(n, dtype=torch.uint8, device=device or torch.device("cuda"))
+    with torch.cuda.device(device):
+        n = token_logprobs_workspace_bytes(rows, vocab, top)
+        if n == 0:
+            raise ValueError("invalid logprobs sizes")
+        return torch.zeros(n, dtype=torch.uint8, device="cuda")
 
 
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None, logprobs: torch.Tensor | None,

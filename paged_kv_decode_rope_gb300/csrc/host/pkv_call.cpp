@@ -11,6 +11,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -142,12 +143,33 @@ void* stream_of(PyObject* o, const at::Tensor& t, const char* name) {
   return reinterpret_cast<void*>(v);
 }
 
+// The device of the call's CUDA tensors, -1 if it has none (what is no CUDA
+// tensor is refused by name where it is read).
+int device_of(PyObject* const* a, Py_ssize_t n) {
+  int device = -1;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    if (a[i] == Py_None || PyLong_Check(a[i]) || PyFloat_Check(a[i]) || !THPVariable_Check(a[i])) continue;
+    const at::Tensor& t = THPVariable_Unpack(a[i]);
+    if (!t.is_cuda()) continue;
+    const int d = t.get_device();
+    if (device >= 0 && d != device)
+      refuse(PyExc_ValueError, "all tensors must be on one device, got cuda:" + std::to_string(device) + " and cuda:" +
+                                   std::to_string(d));
+    device = d;
+  }
+  return device;
+}
+
 // Every function takes exactly `count` positional arguments and returns the
-// library's result. No C++ exception leaves it.
+// library's result, called with the tensors' device current. No C++ exception
+// leaves it.
 template <Py_ssize_t count, typename F>
 PyObject* call(PyObject* const* a, Py_ssize_t n, F body) {
   try {
     if (n != count) refuse(PyExc_TypeError, "expected " + std::to_string(count) + " arguments");
+    const int device = device_of(a, n);
+    c10::cuda::OptionalCUDAGuard guard;
+    if (device >= 0) guard.set_index(static_cast<c10::DeviceIndex>(device));
     return PyLong_FromLong(body(a));
   } catch (const Refused&) {
     return nullptr;

@@ -409,6 +409,7 @@ int paged_gqa_decode_scored(const pkv_pool_t* pool, const float* q_rot, void* ou
   if (!q_rot || !out || !block_tables || !seq_lens || !workspace) return -EINVAL;
   if (!aligned16(q_rot) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return -EINVAL;
+  if (const int rc = pkv::check_pool_device(pool)) return rc;
   const size_t need = paged_gqa_decode_workspace_bytes(batch, num_q_heads, pool->num_kv_heads,
                                                        max_blocks, 0);
   if (need == 0 || workspace_bytes < need) return -EINVAL;
@@ -455,10 +456,8 @@ int paged_gqa_prefill_scored(const pkv_pool_t* pool, const float* q_rot, void* o
     return -EINVAL;
   const size_t need = paged_prefill_workspace_bytes(total_tokens, batch, max_blocks);
   if (need == 0 || workspace_bytes < need) return -EINVAL;
-  int device = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return cuda_fail(e);
-  const int sms = pkv::device_sm_count(device);
+  if (const int rc = pkv::check_pool_device(pool)) return rc;
+  const int sms = pkv::device_sm_count(pool->device);
   if (sms < 1) return -EINVAL;
   pkv::PrefillLaunch a = {};
   a.kv_map = &pool->kv_map;
@@ -486,7 +485,7 @@ int paged_gqa_prefill_scored(const pkv_pool_t* pool, const float* q_rot, void* o
   a.prefix_lens = prefix_lens;
   a.doc_starts = doc_starts;
   a.out_bf16 = out_type == PKV_BF16;
-  e = pkv::launch_prefill_scored(a, static_cast<cudaStream_t>(stream));
+  cudaError_t e = pkv::launch_prefill_scored(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? 0 : cuda_fail(e);
 }
 

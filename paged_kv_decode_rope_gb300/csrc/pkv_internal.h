@@ -1,6 +1,7 @@
 // pkv_internal.h -- host-side interfaces between the C ABI and the kernels.
 #pragma once
 
+#include <cerrno>
 #include <cstddef>
 #include <cstdint>
 
@@ -172,6 +173,18 @@ int device_sm_count(int device);
 
 // Remember a CUDA failure for pkv_last_cuda_error() (calling thread).
 void record_cuda_error(cudaError_t e);
+
+// 0 if the pool's device is the current one, so that what a call launches and
+// asks for its sizes is where the pool is; -EINVAL otherwise.
+inline int check_pool_device(const pkv_pool* pool) {
+  int device = 0;
+  const cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) {
+    record_cuda_error(e);
+    return -EIO;
+  }
+  return device == pool->device ? 0 : -EINVAL;
+}
 
 // Encode a TMA descriptor of the pool (see pkv_pool::kv_map) with boxes of
 // box_rows rows.

@@ -283,6 +283,7 @@ extern "C" int paged_rope_append(pkv_pool_t* pool, const void* q, long long q_st
   if (!q || !k || !v || !q_rot || !slot_map || !positions || !rope_table) return -EINVAL;
   for (const void* x : {q, k, v, static_cast<const void*>(q_rot), rope_table})
     if (reinterpret_cast<uintptr_t>(x) & 15u) return -EINVAL;
+  if (const int rc = check_pool_device(pool)) return rc;
   RopeAppendParams p;
   p.pool = static_cast<uint16_t*>(pool->storage);
   p.num_pages = pool->num_pages;

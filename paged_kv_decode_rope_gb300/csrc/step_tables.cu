@@ -276,6 +276,7 @@ extern "C" int paged_tables_build(pkv_pool_t* pool, const int32_t* start_pos, co
   p.capacity = capacity;
   p.err = pool->d_err;
   if (tables_overlap(p)) return -EINVAL;
+  if (const int rc = check_pool_device(pool)) return rc;
   const size_t smem = tables_smem(batch);
   if (smem > 48u * 1024u) {
     const cudaError_t e = cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
