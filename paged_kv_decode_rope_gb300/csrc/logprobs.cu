@@ -43,7 +43,6 @@
 // split over several CTAs each; the last CTA of a row to finish (a ticket in the
 // workspace) merges the pieces in their order, so the result does not depend
 // on which one it is.
-#include <atomic>
 #include <cerrno>
 #include <climits>
 #include <cmath>
@@ -767,11 +766,8 @@ int token_logprobs(const void* logits, int logits_type, long long row_stride, in
   p.keys = reinterpret_cast<uint64_t*>(ws + at.keys);
   auto kernel = logits_type == PKV_BF16 ? logprobs_kernel<uint16_t> : logprobs_kernel<float>;
   constexpr int kSmem = kLogStages * kStageVectors * 16;
-  static std::atomic<bool> ready[2];
-  if (!ready[logits_type].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e == cudaSuccess) ready[logits_type].store(true, std::memory_order_relaxed);
-  }
+  static DeviceSetup setup[2];
+  e = setup[logits_type]([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
   if (e == cudaSuccess) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -1,6 +1,7 @@
 // pkv_internal.h -- host-side interfaces between the C ABI and the kernels.
 #pragma once
 
+#include <atomic>
 #include <cerrno>
 #include <cstddef>
 #include <cstdint>
@@ -173,6 +174,25 @@ int device_sm_count(int device);
 
 // Remember a CUDA failure for pkv_last_cuda_error() (calling thread).
 void record_cuda_error(cudaError_t e);
+
+// A kernel's set-up before its first launch on a device: the attributes of a
+// function belong to the device that is current when they are set.
+class DeviceSetup {
+  std::atomic<uint64_t> done_{0};  // devices 0 to 63; any other is set up in every call
+
+ public:
+  template <typename F>
+  cudaError_t operator()(F set) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = device < 64 ? 1ull << device : 0;
+    if (done_.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = set();
+    if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
+};
 
 // 0 if the pool's device is the current one, so that what a call launches and
 // asks for its sizes is where the pool is; -EINVAL otherwise.

@@ -18,7 +18,6 @@
 // per step, through a TMA ring; tcgen05 MMAs with fp32 accumulators in tensor
 // memory compute S = Q K^T and O += P V, and four threads per row (16 keys
 // each) run the online softmax on its row of S.
-#include <atomic>
 #include <climits>
 #include <cub/block/block_scan.cuh>
 
@@ -848,9 +847,9 @@ cudaError_t launch_all(const PrefillLaunch& a, const PrefillLayout& l, cudaStrea
   p.qscale = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.err = a.err;
   const int smem = static_cast<int>(C::kBytes + 1024);  // + alignment to 1 KiB
-  static std::atomic<bool> attr_set[9];
-  if (!attr_set[G].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(prefill_tc_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static DeviceSetup setup;
+  e = setup([&] {
+    cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // The warpgroups' register shares must fit in what the launch gives the
     // CTA (the compiler's count a thread x its threads), or the softmax
@@ -858,10 +857,11 @@ cudaError_t launch_all(const PrefillLaunch& a, const PrefillLayout& l, cudaStrea
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, prefill_tc_kernel<G>);
     if (e != cudaSuccess) return e;
-    if (128 * C::kIssueRegs + C::kSoftmaxThreads * C::kSoftmaxRegs > C::kThreads * fa.numRegs)
-      return cudaErrorInvalidConfiguration;
-    attr_set[G].store(true, std::memory_order_relaxed);
-  }
+    return 128 * C::kIssueRegs + C::kSoftmaxThreads * C::kSoftmaxRegs > C::kThreads * fa.numRegs
+               ? cudaErrorInvalidConfiguration
+               : cudaSuccess;
+  });
+  if (e != cudaSuccess) return e;
   const size_t n_ctas = grid_x * static_cast<size_t>(a.num_kv_heads);
   if (n_ctas > 0x7fffffffu) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(n_ctas));

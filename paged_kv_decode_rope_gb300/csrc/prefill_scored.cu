@@ -49,7 +49,6 @@
 // hand registers to them, issue: 8 the K copies, 11 the V copies, 9 the score
 // products, 10 the P V products, each as soon as its operands and buffers are
 // free. Every wait is bounded.
-#include <atomic>
 #include <climits>
 
 #include "f32x2.cuh"
@@ -874,8 +873,8 @@ template <int G, bool kPair>
 cudaError_t launch(const PrefillLaunch& a, int4* tiles, int* counts, cudaStream_t stream) {
   using C = Cfg<G>;
   const int smem = static_cast<int>(C::kBytes + 1024);  // + alignment to 1 KiB
-  static std::atomic<bool> ready;
-  if (!ready.load(std::memory_order_relaxed)) {
+  static DeviceSetup setup;
+  cudaError_t e = setup([&] {
     cudaError_t e = cudaFuncSetAttribute(prefill_scored_kernel<G, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // The warpgroups' register shares must fit in what the launch gives the
@@ -884,10 +883,11 @@ cudaError_t launch(const PrefillLaunch& a, int4* tiles, int* counts, cudaStream_
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, prefill_scored_kernel<G, kPair>);
     if (e != cudaSuccess) return e;
-    if (128 * C::kIssueRegs + C::kSoftmaxThreads * C::kSoftmaxRegs > C::kThreads * fa.numRegs)
-      return cudaErrorInvalidConfiguration;
-    ready.store(true, std::memory_order_relaxed);
-  }
+    return 128 * C::kIssueRegs + C::kSoftmaxThreads * C::kSoftmaxRegs > C::kThreads * fa.numRegs
+               ? cudaErrorInvalidConfiguration
+               : cudaSuccess;
+  });
+  if (e != cudaSuccess) return e;
   const size_t capacity = static_cast<size_t>(a.total_tokens + C::kTokens - 1) / C::kTokens + a.batch;
   const size_t units = capacity * static_cast<size_t>(a.num_kv_heads);
   if (units > 0x7fff0000u) return cudaErrorInvalidValue;
@@ -896,7 +896,7 @@ cudaError_t launch(const PrefillLaunch& a, int4* tiles, int* counts, cudaStream_
   prefill_scored_plan_kernel<<<1, kPlanThreads, 0, stream>>>(
       a.cu_tokens, a.start_pos, a.batch, a.total_tokens, C::kTokens, static_cast<int>(capacity), a.window,
       a.doc_starts, grid, tiles, counts, a.err);
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   constexpr double log2e = 1.4426950408889634;
   ScoredParams p = {};

@@ -23,4 +23,19 @@ int main() {
       std::printf("pool on %d, current %d: %d\n", pool.device, g_device, pkv::check_pool_device(&pool));
   g_get_device = cudaErrorNoDevice;
   std::printf("no device: %d\n", pkv::check_pool_device(&pool));
+  g_get_device = cudaSuccess;
+
+  // a kernel's attributes are set once on each device, and again after a failure
+  int calls[2] = {0, 0};
+  cudaError_t answer = cudaErrorInvalidValue;
+  pkv::DeviceSetup setup;
+  for (int round = 0; round < 3; ++round, answer = cudaSuccess)
+    for (g_device = 0; g_device < 2; ++g_device) {
+      const int device = g_device;
+      const cudaError_t e = setup([&] {
+        ++calls[device];
+        return answer;
+      });
+      std::printf("set-up %d on %d: %d, set %d times\n", round, device, static_cast<int>(e), calls[device]);
+    }
 }

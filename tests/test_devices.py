@@ -25,9 +25,20 @@ def host_program(tmp_path, name):
 
 
 def test_a_pool_of_another_device_is_refused(tmp_path):
-    assert host_program(tmp_path, "host_device") == [
+    assert host_program(tmp_path, "host_device")[:6] == [
         "pool on 0, current 0: 0", "pool on 0, current 1: -22", "pool on 1, current 0: -22", "pool on 1, current 1: 0",
-        f"recorded {100}", "no device: -5"]
+        "recorded 100", "no device: -5"]
+
+
+def test_a_kernel_is_set_up_on_every_device(tmp_path):
+    assert host_program(tmp_path, "host_device")[6:] == [
+        "set-up 0 on 0: 1, set 1 times", "set-up 0 on 1: 1, set 1 times", "set-up 1 on 0: 0, set 2 times",
+        "set-up 1 on 1: 0, set 2 times", "set-up 2 on 0: 0, set 2 times", "set-up 2 on 1: 0, set 2 times"]
+    # and no kernel keeps that it is set up without the device
+    for name in ("logprobs.cu", "prefill.cu", "prefill_scored.cu"):
+        with open(os.path.join(build.CSRC, name)) as f:
+            text = f.read()
+        assert "DeviceSetup" in text and "static std::atomic<bool>" not in text, name
 
 
 def calls():
