@@ -590,8 +590,9 @@ size_t token_logprobs_workspace_bytes(int rows, int vocab, int top);
  *            top_logprobs fp32 [rows][top] (NULL when top is 0)
  *   workspace  device memory of at least token_logprobs_workspace_bytes(),
  *            256-byte aligned, ZERO-FILLED before its first use (each call
- *            leaves what it needs to be zero at zero). Calls that share a
- *            workspace must not overlap on the GPU.
+ *            leaves what it needs to be zero at zero, unless it ends with
+ *            PKV_ERR_TIMEOUT). Calls that share a workspace must not overlap
+ *            on the GPU.
  * A logit of -inf is a token of probability 0. A row that holds +inf or NaN,
  * or only -inf, has no distribution: its logprobs, entropy and top_logprobs
  * are NaN; top_ids still follow the order of its logits, NaN taken as -inf.
@@ -600,6 +601,23 @@ int token_logprobs(const void *logits, int logits_type, long long row_stride, in
                    float scale, const int32_t *targets, int top, float *logprobs, float *entropy,
                    int32_t *top_ids, float *top_logprobs, void *workspace, size_t workspace_bytes,
                    void *stream);
+
+/*
+ * token_logprobs has no pool; its error word is in the workspace. A wait that
+ * gives up sets PKV_ERR_TIMEOUT there. That call's results are incomplete: what was
+ * not worked out is NaN, with top_ids 0. So is every row of later calls on the
+ * workspace, until the word is reset.
+ *   token_logprobs_get_error       synchronises and reads the word; reset != 0
+ *                                  makes the workspace as new
+ *   token_logprobs_set_wait_limit  bound of a wait in polls, for later calls of
+ *                                  the process; 0 gives up at once. The
+ *                                  default (previous, if not NULL, gets the
+ *                                  bound that was set) is far above what a copy
+ *                                  takes.
+ */
+int token_logprobs_get_error(void *workspace, int *bits, int reset);
+int token_logprobs_set_wait_limit(uint32_t polls, uint32_t *previous);
+
 
 /*
  * Read the pool's device error word (PKV_ERR_* bits) into *bits; with reset

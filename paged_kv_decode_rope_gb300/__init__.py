@@ -62,6 +62,8 @@ from ._binding import (  # noqa: F401
     pkv_get_error,
     pkv_last_cuda_error,
     token_logprobs,
+    token_logprobs_get_error,
+    token_logprobs_set_wait_limit,
     token_logprobs_workspace_bytes,
 )
 from .rope import rope_frequencies  # noqa: F401

@@ -61,6 +61,8 @@ _SIGNATURES = {
                                       _vp]),
     "token_logprobs_workspace_bytes": (_sz, [_i, _i, _i]),
     "token_logprobs": (_i, [_vp, _i, _ll, _i, _i, _f, _vp, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "token_logprobs_get_error": (_i, [_vp, ctypes.POINTER(_i), _i]),
+    "token_logprobs_set_wait_limit": (_i, [ctypes.c_uint32, ctypes.POINTER(ctypes.c_uint32)]),
     "pkv_get_error": (_i, [_vp, ctypes.POINTER(_i), _i]),
     "pkv_last_cuda_error": (_i, []),
     # include/pkv_sched.h (host only)
@@ -597,6 +599,26 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None, logprobs:
                                                     workspace, scale, stream)
     if rc:
         _refused("token_logprobs", rc)
+
+
+def token_logprobs_get_error(workspace: torch.Tensor, reset: bool = False) -> int:
+    """The error word of token_logprobs' workspace (synchronises): ERR_TIMEOUT
+    after a call that gave up a wait. Its rows that were not worked out, and
+    all rows of later calls on the workspace, are NaN until a reset."""
+    bits, at = _i(0), _dev(workspace, torch.uint8, "workspace", 1)
+    with torch.cuda.device(workspace.device):
+        if workspace.numel() < token_logprobs_workspace_bytes(1, 1, 0):
+            raise ValueError("workspace too small")
+        _check("token_logprobs_get_error", lib().token_logprobs_get_error(at, ctypes.byref(bits), int(reset)))
+    return bits.value
+
+
+def token_logprobs_set_wait_limit(polls: int) -> int:
+    """Bound of token_logprobs' waits, in polls, for later calls of the process
+    (0: give up at once, setting ERR_TIMEOUT). Returns the previous bound."""
+    prev = ctypes.c_uint32(0)
+    _check("token_logprobs_set_wait_limit", lib().token_logprobs_set_wait_limit(int(polls), ctypes.byref(prev)))
+    return prev.value
 
 
 def pkv_get_error(pool: KVPool, reset: bool = False) -> int:

@@ -11,7 +11,7 @@
 // shared-memory stages and runs ahead into the next row while the others pick
 // the alternatives of this one, so that the memory never idles (a CTA a row,
 // loading as it went: 128 us for 2048 rows of 128256 bf16, 60% of the copy
-// bandwidth; now 112 us, 4.70 TB/s, 69%). Rows are handed out from a counter:
+// bandwidth; now 114 us, 4.63 TB/s, 68%). Rows are handed out from a counter:
 // with a fixed share for every CTA the slowest SM's memory path set the time
 // (33% over the median's). What bounds it is that stream together with the
 // issue slots of its arithmetic (unpack, difference, product, exp2, two sums
@@ -43,6 +43,14 @@
 // split over several CTAs each; the last CTA of a row to finish (a ticket in the
 // workspace) merges the pieces in their order, so the result does not depend
 // on which one it is.
+//
+// Every wait is bounded. When one gives up, the computing warps of its CTA leave
+// together (a barrier tells all of them), the workspace's error word says so and
+// the CTA makes every row NaN; other CTAs may write theirs later. The counter and
+// the tickets are then left as they are, so a call that finds the error word set
+// writes NaN everywhere and touches neither. (All this takes 1.5% of the 2048
+// rows: 113.6 us against 111.9.)
+#include <atomic>
 #include <cerrno>
 #include <climits>
 #include <cmath>
@@ -94,6 +102,8 @@ struct LogprobsParams {
   int splits;          // pieces of each row after them
   int split_vectors;   // vectors of such a piece
   int pieces;          // of all rows
+  int* error;          // PKV_ERR_TIMEOUT, from this call or one before it
+  uint32_t polls;      // bound of the waits
   int* counter;        // pieces handed out past the first round, zero between calls
   int* tickets;        // [split rows], zero between calls
   float4* sums;        // [split pieces] {m, S, Z, -}
@@ -133,6 +143,19 @@ __device__ __forceinline__ uint64_t merge32(uint64_t a, uint64_t b, int lane) {
 // A barrier of the CTA's computing warps.
 __device__ __forceinline__ void compute_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kLogThreads) : "memory");
+}
+// The same; true if `mine` is true in all of their threads.
+__device__ __forceinline__ bool compute_all(bool mine) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(mine)), "n"(kLogThreads)
+      : "memory");
+  return all != 0;
 }
 // The 32 largest of the first `lists` warps' sorted lists, in warp 0 (all
 // computing threads call it; s_list is free again after the caller's next
@@ -313,12 +336,13 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
     for (int n = 0; !failed; ++n) {
       int piece = blockIdx.x;
       if (n > 0) {
+        if (n == 1 && __ldcg(p.error) != 0) break;  // (the computing warps leave after the first piece)
         const int v = atomicAdd(p.counter, 1);
         piece = static_cast<int>(gridDim.x) + v;
         if (v == pieces - 1) *p.counter = 0;  // every CTA has had its last answer: ready for the next call
       }
       if (piece >= pieces) piece = -1;
-      if (n >= 2 && !mbar_wait_bounded(smem_addr(&piece_empty[n & 1]), ((n >> 1) - 1) & 1)) {
+      if (n >= 2 && !mbar_wait_bounded(smem_addr(&piece_empty[n & 1]), ((n >> 1) - 1) & 1, p.polls)) {
         failed = true;
         break;
       }
@@ -328,7 +352,7 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
       const Piece<T> r(p, piece);
       for (int c = r.v0; c < r.v1; c += kStageVectors, ++chunk) {
         const int st = chunk % kLogStages, use = chunk / kLogStages;
-        if (use > 0 && !mbar_wait_bounded(smem_addr(&empty[st]), (use - 1) & 1)) {
+        if (use > 0 && !mbar_wait_bounded(smem_addr(&empty[st]), (use - 1) & 1, p.polls)) {
           failed = true;
           break;
         }
@@ -344,18 +368,27 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
         }
       }
     }
+    if (failed) atomicOr(p.error, PKV_ERR_TIMEOUT);
     // let the copies still in flight land before shared memory goes away
     for (int k = max(0, chunk - kLogStages); k < chunk; ++k)
       mbar_wait_bounded(smem_addr(&full[k % kLogStages]), (k / kLogStages) & 1);
     return;
   }
 
+  // The computing warps leave together, at a barrier after a piece's stream, so
+  // what a warp finds on its own (that no piece or no copy came) only lets it run
+  // through to there without waiting again.
+  bool good;
   for (int n = 0;; ++n) {
-    if (!mbar_wait_bounded(smem_addr(&piece_full[n & 1]), (n >> 1) & 1)) break;  // (only after the copies gave up)
-    const int piece = s_piece[n & 1];
+    const bool lost =
+        __any_sync(kFull, !mbar_wait_bounded(smem_addr(&piece_full[n & 1]), (n >> 1) & 1, p.polls));
+    const int piece = lost ? static_cast<int>(blockIdx.x) : s_piece[n & 1];
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&piece_empty[n & 1]));
-    if (piece < 0) break;
+    if (piece < 0) {  // no more
+      good = compute_all(true);
+      break;
+    }
     const Piece<T> r(p, piece);
     const int row = r.row, v0 = r.v0, v1 = r.v1;
     // ---- the stream ----
@@ -402,10 +435,10 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
         z2 = fma_f32x2(e2, y2, z2);
       }
     };
-    bool late = false;  // a copy did not come: its vectors count as NaN
+    uint32_t polls = lost ? 0 : p.polls;  // 0: a copy did not come, stages are not given back
     for (int c = v0; c < v1; c += kStageVectors, ++chunk) {
       const int st = chunk % kLogStages;
-      if (!mbar_wait_bounded(smem_addr(&full[st]), (chunk / kLogStages) & 1)) late = true;
+      if (!mbar_wait_bounded(smem_addr(&full[st]), (chunk / kLogStages) & 1, polls)) polls = 0;
       const uint32_t src = smem_addr(s_ring) + (st * kStageVectors + tid) * 16;
       if (c >= r.whole0 && c + kStageVectors <= min(v1, r.whole1)) {
 #pragma unroll
@@ -419,7 +452,7 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&empty[st]));
+      if (lane == 0 && polls > 0) mbar_arrive(smem_addr(&empty[st]));
     }
 
     // ---- the sums and the K best of the CTA's piece ----
@@ -444,7 +477,8 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
         s_count = 0;
       }
     }
-    compute_sync();
+    good = compute_all(polls > 0 && (n > 0 || tid > 0 || __ldcg(p.error) == 0));
+    if (!good) break;
     Sums all;
     all.m = s_ref[0];
     uint32_t least = s_least[0];
@@ -455,7 +489,7 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
     }
     {
       const float2 s = unpack_f32x2(s2), z = unpack_f32x2(z2);
-      all.s = late ? NAN : s.x + s.y;
+      all.s = s.x + s.y;
       all.z = z.x + z.y;
       if (all.m == -INFINITY || all.m > kHuge) {  // rare
         atomicMax(&s_top, mine);
@@ -667,17 +701,28 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
     }
     compute_sync();  // the shared arrays are free for the next piece
   }
+  if (!good) {
+    if (tid == 0) atomicOr(p.error, PKV_ERR_TIMEOUT);
+    for (long long i = tid; i < p.rows; i += kLogThreads) {
+      if (p.targets) p.logprobs[i] = NAN;
+      if (p.entropy) p.entropy[i] = NAN;
+    }
+    for (long long i = tid; i < static_cast<long long>(p.rows) * p.top; i += kLogThreads) {
+      p.top_ids[i] = 0;  // a token's id all the same, so that what looks it up stays in range
+      p.top_logprobs[i] = NAN;
+    }
+  }
 }
 
-// The workspace: counter and tickets, then the split pieces' sums and keys. Its
-// places depend on the GPU alone (fewer rows are split than CTAs run at once, into
-// no more pieces than that), not on a call's sizes, so a call finds its
-// counter and tickets where every other call left them at zero.
+// The workspace: error word, counter and tickets, then the split pieces' sums
+// and keys. Its places depend on the GPU alone (fewer rows are split than CTAs
+// run at once, into no more pieces than that), not on a call's sizes, so a call
+// finds its counter and tickets where every other call left them at zero.
 struct Workspace {
-  size_t sums, keys, bytes;  // offsets; tickets follow the counter at 0
+  size_t sums, keys, bytes;  // offsets; error word, counter and tickets from 0 on
   explicit Workspace(int ctas) {
     auto align256 = [](size_t n) { return (n + 255) / 256 * 256; };
-    sums = align256(sizeof(int) * (static_cast<size_t>(ctas) + 1));
+    sums = align256(sizeof(int) * (static_cast<size_t>(ctas) + 2));
     keys = sums + align256(sizeof(float4) * ctas);
     bytes = keys + sizeof(uint64_t) * kTop * ctas;
   }
@@ -700,10 +745,39 @@ Cut cut(int rows, long long vectors, int ctas) {
   return n < 2 ? Cut{rows, 1} : Cut{rows - rest, static_cast<int>(n)};
 }
 
+// A poll that finds nothing takes 4 us, so about a second.
+std::atomic<uint32_t> g_wait_polls{1u << 18};
+
 }  // namespace
 }  // namespace pkv
 
 extern "C" {
+
+int token_logprobs_set_wait_limit(uint32_t polls, uint32_t* previous) {
+  const uint32_t before = pkv::g_wait_polls.exchange(polls);
+  if (previous) *previous = before;
+  return 0;
+}
+
+int token_logprobs_get_error(void* workspace, int* bits, int reset) {
+  using namespace pkv;
+  if (!workspace || !bits || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return -EINVAL;
+  int device = 0, v = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpy(&v, workspace, sizeof(int), cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess && reset) {
+    const int sms = device_sm_count(device);
+    if (sms < 1) return -EIO;
+    e = cudaMemset(workspace, 0, Workspace(kLogCtas * sms).sums);
+  }
+  if (e != cudaSuccess) {
+    record_cuda_error(e);
+    return -EIO;
+  }
+  *bits = v;
+  return 0;
+}
 
 size_t token_logprobs_workspace_bytes(int rows, int vocab, int top) {
   using namespace pkv;
@@ -759,7 +833,9 @@ int token_logprobs(const void* logits, int logits_type, long long row_stride, in
   if (pieces > 0x7fff0000ll) return -EINVAL;
   p.pieces = static_cast<int>(pieces);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.counter = reinterpret_cast<int*>(ws);
+  p.error = reinterpret_cast<int*>(ws);
+  p.polls = g_wait_polls.load(std::memory_order_relaxed);
+  p.counter = p.error + 1;
   p.tickets = p.counter + 1;
   const Workspace at(ctas);
   p.sums = reinterpret_cast<float4*>(ws + at.sums);
