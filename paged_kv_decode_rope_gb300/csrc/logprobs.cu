@@ -400,7 +400,9 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
     float best = -INFINITY, next = -INFINITY;  // the largest logit, and of the vectors without it
     int best_v = v0 + tid;
     uint4 best_w = make_uint4(0u, 0u, 0u, 0u);
-    // the target's logit, wanted at the end
+    // the error word and the target's logit, wanted at the end (by reading the word
+    // there 1 row took 9.9 us instead of 9.6)
+    const int error = tid == 0 ? __ldcg(p.error) : 0;
     const int target = p.targets && tid == 0 ? p.targets[row] : -1;
     const float target_x =
         target >= 0 && target < p.vocab ? V::value(V::raw(r.base + static_cast<size_t>(target) * sizeof(T))) : NAN;
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(kLogBlock, kLogCtas) logprobs_kernel(const Log
         s_count = 0;
       }
     }
-    good = compute_all(polls > 0 && (n > 0 || tid > 0 || __ldcg(p.error) == 0));
+    good = compute_all(polls > 0 && error == 0);
     if (!good) break;
     Sums all;
     all.m = s_ref[0];
