@@ -15,6 +15,8 @@ import threading
 
 import torch
 
+from . import build
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(_HERE, "libpkv.so")
 
@@ -471,9 +473,10 @@ def _native():
         if _call_module is not None:
             return _call_module
     L = lib()
-    path = os.path.join(_HERE, "_pkv_call.so")
+    path = build.call_module()
     if not os.path.exists(path):
-        raise RuntimeError(f"{path} is not built; run paged_kv_decode_rope_gb300.build.build()")
+        raise RuntimeError(f"{path} is not built for this Python and torch; run "
+                           "paged_kv_decode_rope_gb300.build.build()")
     spec = importlib.util.spec_from_file_location("_pkv_call", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)

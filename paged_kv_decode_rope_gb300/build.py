@@ -1,25 +1,27 @@
 """Build the pkv CUDA library (libpkv.so) in-tree for sm_103a.
 
 Each translation unit is compiled in parallel with nvcc, then linked into one
-shared library next to this file. Beside it the CPython module _pkv_call.so
+shared library next to this file. Beside it the CPython module _pkv_call
 (csrc/host/pkv_call.cpp, the argument checks of the serving calls) is built with
-the host compiler against the installed torch. Rebuilds only when a source is
-newer than what it makes.
+the host compiler against the installed torch, under a name that says which
+Python and torch that was. Rebuilds only when a source is newer than what it
+makes.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
 import os
+import re
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIBRARY = os.path.join(HERE, "libpkv.so")
 CALL_SOURCE = os.path.join(CSRC, "host", "pkv_call.cpp")
-CALL_MODULE = os.path.join(HERE, "_pkv_call.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -50,19 +52,28 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def call_module() -> str:
+    """Where the CPython module for the Python and torch that run this is. It is
+    bound to torch's C++ interface, so every torch (its version, the commit it
+    was built from, its C++ ABI) has a file of its own and none is loaded into another."""
+    import torch
+    tag = (f"{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}-{str(torch.version.git_version)[:8]}"
+           f"-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}")
+    return os.path.join(HERE, "_pkv_call." + re.sub(r"[^\w.+-]", "_", tag) + ".so")
+
+
 def build_call(force: bool = False) -> str:
     """The CPython module, against the Python and torch that run this."""
+    module = call_module()
     inputs = [CALL_SOURCE, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and os.path.exists(CALL_MODULE) and \
-            all(os.path.getmtime(f) <= os.path.getmtime(CALL_MODULE) for f in inputs):
-        return CALL_MODULE
-    import sysconfig
+    if not force and os.path.exists(module) and all(os.path.getmtime(f) <= os.path.getmtime(module) for f in inputs):
+        return module
 
     import torch
     root = os.path.dirname(torch.__file__)
     include = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")]
-    tmp = CALL_MODULE + f".{os.getpid()}.tmp"
+    tmp = module + f".{os.getpid()}.tmp"
     cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in include),
            CALL_SOURCE, "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
@@ -70,8 +81,8 @@ def build_call(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compiler failed for {CALL_SOURCE}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALL_MODULE)
-    return CALL_MODULE
+    os.replace(tmp, module)
+    return module
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
