@@ -54,6 +54,7 @@
 #include "f32x2.cuh"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "score_cap.cuh"
 #include "tc05.cuh"
 
 namespace pkv {
@@ -65,10 +66,13 @@ constexpr int kSBufs = 2;
 constexpr uint32_t kTmemCols = 256;  // two S buffers of 64 columns, O (64), l (16 equal columns)
 constexpr int kCtas = 2;             // CTAs a SM
 
-// tanh(x) on |x| <= kPolyMax as x (c0 + c1 x^2 + c2 x^4) with the smallest
-// largest error (1.7e-7, found by exchanging the error's extrema): four paired
-// fp32 operations for two scores. Elsewhere cap tanh(x) = cap - 2 cap / (2^t +
-// 1) with t = 2 log2(e) x, two special-function operations a score.
+// tanh(x) on |x| <= kPolyMax. Where the output is bf16, as x (c0 + c1 x^2 + c2
+// x^4) with the smallest largest error (1.7e-7, found by exchanging the error's
+// extrema): four paired fp32 operations for two scores. That is up to 4e-6 of
+// a score, all in one direction, which shows where the output is fp32 (kPair), so
+// there it is the polynomial of score_cap.cuh with a term more (1e-8 of a score).
+// Elsewhere cap tanh(x) = cap - 2 cap / (2^t + 1) with t = 2 log2(e) x, two
+// special-function operations a score.
 constexpr double kPolyMax = 0.3;
 constexpr double kPoly[3] = {0.999996010, -0.332974797, 0.125225911};
 
@@ -84,7 +88,7 @@ struct ScoredParams {
   long long num_pages;
   float qscale;        // what a query is multiplied by: scores in base 2, or t when capped
   float cap;           // softcap * log2(e), 0: none
-  float poly[3];       // cap tanh as a polynomial of t: t (poly[0] + poly[1] t^2 + poly[2] t^4)
+  float poly[4];       // cap tanh as a polynomial of t: t (poly[0] + poly[1] t^2 + poly[2] t^4 + poly[3] t^6)
   const int32_t* cu_tokens;    // [batch + 1]
   const int32_t* start_pos;    // [batch]
   const int32_t* prefix_lens;  // [batch] or null
@@ -561,13 +565,16 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
           if (p.cap > 0.f) {
             const uint64_t c0 = f32x2(p.poly[0], p.poly[0]), c1 = f32x2(p.poly[1], p.poly[1]);
             const uint64_t c2 = f32x2(p.poly[2], p.poly[2]);
+            [[maybe_unused]] const uint64_t c3 = f32x2(p.poly[3], p.poly[3]);
             float um = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const uint64_t x = f32x2(sv[2 * i], sv[2 * i + 1]), u = mul_f32x2(x, x);
               const float2 uf = unpack_f32x2(u);
               um = fmax3(um, uf.x, uf.y);
-              const float2 v = unpack_f32x2(fma_f32x2(fma_f32x2(fma_f32x2(c2, u, c1), u, c0), x, off[i & 1]));
+              uint64_t h = c2;
+              if constexpr (kPair) h = fma_f32x2(c3, u, c2);
+              const float2 v = unpack_f32x2(fma_f32x2(fma_f32x2(fma_f32x2(h, u, c1), u, c0), x, off[i & 1]));
               sv[2 * i] = v.x;
               sv[2 * i + 1] = v.y;
             }
@@ -587,7 +594,8 @@ __global__ void __launch_bounds__(Cfg<G>::kThreads, kCtas)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const float u = x[i] * x[i], o = unpack_f32x2(off[i >> 1]).x;
-                  const float near = fmaf(fmaf(fmaf(p.poly[2], u, p.poly[1]), u, p.poly[0]), x[i], o);
+                  const float h = kPair ? fmaf(p.poly[3], u, p.poly[2]) : p.poly[2];
+                  const float near = fmaf(fmaf(fmaf(h, u, p.poly[1]), u, p.poly[0]), x[i], o);
                   const float far = fmaf(-2.f * p.cap, fast_rcp(fast_exp2(x[i]) + 1.f), p.cap) + o;
                   x[i] = u <= static_cast<float>(kMostT * kMostT) ? near : far;
                 }
@@ -912,9 +920,14 @@ cudaError_t launch(const PrefillLaunch& a, int4* tiles, int* counts, cudaStream_
   p.num_pages = a.num_pages;
   p.qscale = static_cast<float>(a.softcap > 0.f ? 2.0 * a.scale / a.softcap * log2e : a.scale * log2e);
   p.cap = static_cast<float>(a.softcap * log2e);
-  double step = 1.0 / (2.0 * log2e);  // x = t / (2 log2 e)
-  for (int i = 0; i < 3; ++i, step /= 4.0 * log2e * log2e)
-    p.poly[i] = static_cast<float>(a.softcap * log2e * kPoly[i] * step);
+  if constexpr (kPair) {
+    const ScoreCap cap = make_score_cap(a.softcap);
+    for (int i = 0; i < 4; ++i) p.poly[i] = cap.c[i];
+  } else {
+    double step = 1.0 / (2.0 * log2e);  // x = t / (2 log2 e)
+    for (int i = 0; i < 3; ++i, step /= 4.0 * log2e * log2e)
+      p.poly[i] = static_cast<float>(a.softcap * log2e * kPoly[i] * step);
+  }
   p.cu_tokens = a.cu_tokens;
   p.start_pos = a.start_pos;
   p.prefix_lens = a.prefix_lens;

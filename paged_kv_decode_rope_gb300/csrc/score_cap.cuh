@@ -1,4 +1,5 @@
-// score_cap.cuh -- the tanh cap of the scored decodes.
+// score_cap.cuh -- the tanh cap of the scored decodes, and its polynomial for the
+// scored prefill.
 #pragma once
 
 #include "pkv_device.cuh"
