@@ -514,10 +514,11 @@ def paged_rope_table_build_freqs(inv_freq, num_positions: int, table: torch.Tens
                                  stream=None) -> None:
     """The RoPE table of positions 0 .. num_positions-1 for given inverse
     frequencies (up to 32 numbers, see rope_frequencies), cos and sin
-    multiplied by magnitude."""
+    multiplied by magnitude, into a table of exactly as many rows
+    (alloc_rope_table)."""
     inv_freq = [float(f) for f in inv_freq]
-    if table.numel() < num_positions * ROPE_TABLE_BYTES_PER_ROW:
-        raise ValueError("rope table too small")
+    if table.numel() != num_positions * ROPE_TABLE_BYTES_PER_ROW:  # its size says to its readers where the parts are
+        raise ValueError(f"table must hold num_positions = {num_positions} rows, got {rope_table_rows(table)}")
     at = _dev(table, torch.uint8, "table", 1)
     with torch.cuda.device(table.device):
         rc = lib().paged_rope_table_build_freqs((_d * len(inv_freq))(*inv_freq), len(inv_freq), float(magnitude),
