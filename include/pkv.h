@@ -462,7 +462,8 @@ int paged_tables_build(pkv_pool_t *pool, const int32_t *start_pos, const int32_t
  * magnitude 1 it is the table of paged_rope_table_build. Scaled rotary
  * positions (interpolated, by wavelength band, with an attention factor) are
  * such frequencies and magnitudes.
- *   inv_freq  HOST pointer, double [num_freqs], finite; 1 <= num_freqs <= 32
+ *   inv_freq  HOST pointer, double [num_freqs], finite, every angle below 2^52;
+ *             1 <= num_freqs <= 32
  *   magnitude finite
  */
 int paged_rope_table_build_freqs(const double *inv_freq, int num_freqs, double magnitude,

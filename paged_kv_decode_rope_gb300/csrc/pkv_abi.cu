@@ -286,7 +286,8 @@ int paged_rope_table_build_freqs(const double* inv_freq, int num_freqs, double m
     return -EINVAL;
   double inv[PKV_HEAD_DIM / 2] = {};
   for (int j = 0; j < num_freqs; ++j) {
-    if (!std::isfinite(inv_freq[j])) return -EINVAL;
+    // (rope_cos_or_sin_cr takes angles below 2^52)
+    if (!std::isfinite(inv_freq[j]) || !(std::fabs(inv_freq[j]) * (num_positions - 1) < 0x1p52)) return -EINVAL;
     inv[j] = inv_freq[j];
   }
   cudaError_t e = pkv::launch_rope_table(nullptr, num_positions, inv, magnitude, table,
