@@ -507,7 +507,7 @@ int paged_rope_append(pkv_pool_t *pool, const void *q, long long q_stride, const
  */
 typedef struct pkv_scoring {
   float scale;               /* softmax scale, finite */
-  float softcap;             /* 0: scores are not capped; otherwise > 0, finite */
+  float softcap;             /* 0: scores are not capped; otherwise > 0, at most 1e30 and at least 1e-20 |scale| */
   const float *alibi_slopes; /* fp32 [num_q_heads] on the device, or NULL */
   int window;                /* 0: no window; otherwise the last `window` positions, itself included */
 } pkv_scoring_t;

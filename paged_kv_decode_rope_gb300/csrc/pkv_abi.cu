@@ -40,11 +40,12 @@ bool decode_shape_ok(const pkv_pool_t* pool, int batch, int num_q_heads, int max
   return true;
 }
 
-// A scoring whose folded query scale is a finite fp32 number.
+// A scoring whose folded query scale, scale / softcap, leaves a query times it in
+// the range of a bf16 pair: the lower part a normal number, sums of products
+// finite.
 bool scoring_ok(const pkv_scoring_t* s) {
-  if (!s || !std::isfinite(s->scale) || !std::isfinite(s->softcap) || s->softcap < 0.f || s->window < 0)
-    return false;
-  return s->softcap == 0.f || std::isfinite(3.f * s->scale / s->softcap);
+  if (!s || !std::isfinite(s->scale) || !(s->softcap >= 0.f && s->softcap <= 1e30f) || s->window < 0) return false;
+  return s->softcap == 0.f || std::fabs(s->scale) <= 1e20f * s->softcap;
 }
 
 bool out_type_ok(int type) { return type == PKV_BF16 || type == PKV_F32; }
