@@ -26,15 +26,19 @@
 // The reference maximum of a row moves only when a score passes it by more than
 // kSlack (base 2), so P <= 2^kSlack.
 //
-// Measured, 4 chunks of 2048 tokens, 32 + 8 heads: with a window of 1024 (51.6
-// GFLOP) 132 us with a cap (391 TFLOP/s), 115 without, 214 with a cap whose
-// scores pass kPolyMax; over all keys 133 us, 155 with a cap, 141 with a
-// distance bias, 150 with fp32 out.
+// Measured in graph replays, 4 chunks of 2048 tokens, 32 + 8 heads, bf16 out and
+// (fp32 out): with a window of 1024 (51.6 GFLOP) 130 us (152) with a cap, 396
+// TFLOP/s, 114 (127) without; 234 (265) with a cap of 50 and scores of a standard
+// deviation of 16, most steps of which hold one past kPolyMax; over all keys 133
+// us (150), 153 (182) with a cap, 141 with a distance bias, 144 with a two-way
+// prefix of 512, 164 with both.
 //
-// What bounds it: the softmax warps' instructions (a step of 128 x 64 scores
-// takes an SM some 1450 cycles with a cap and 1280 without, about 420
-// instructions a warp; 62% of the cycles issue one, the special-function pipe is
-// 18% busy), and around it those of a tile's start and end, some 3700 cycles. With
+// What bounds it: the softmax warps. A step of 128 x 64 scores takes an SM some
+// 1450 cycles with a cap and 1280 without, about 420 instructions a warp; 62% of
+// the cycles issue one (the special-function pipe is 18% busy), and in the others
+// the warps wait, for tensor memory and for one another's barriers (1.38 are
+// ready in a cycle). Around the steps come those of a tile's start and end, some
+// 3700 cycles. With
 // a CTA a tile these took 13,000 of the 20,000 cycles of a
 // tile of three steps (window 128): launch, tensor memory, tile, query rows,
 // first keys, last product, epilogue, one after the other. So CTAs stay, two on

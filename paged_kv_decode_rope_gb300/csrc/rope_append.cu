@@ -14,14 +14,16 @@
 // token and computes next to nothing, so memory bounds it, and what it takes
 // is bytes in flight: the cos and sin of a token depend on its position, and a
 // CTA a token spent its life waiting for that chain (48 us for 8192 tokens of
-// 32 + 8 heads, 42% of the copy bandwidth; now 25.4 us, 5.36 TB/s, 79%). So
+// 32 + 8 heads, 42% of the copy bandwidth; now 25.4 us in graph replays, 5.36
+// TB/s, 79%, and 27 as calls). So
 // CTAs stay and stream units (a token, up to kUnitRows of its rows) through a
 // ring of kRopeStages shared-memory stages: one warp issues bulk copies of the
 // units' rows, reads their positions and slots ahead, and copies their table
 // rows when it knows them; kRopeWarps warps rotate and store. Eight threads
 // hold a head's row, 8 dims each: 4 whole pairs (rot_dim is a multiple of 8),
 // the same ones in every row it takes, or 8 dims that pass through. Every wait
-// is bounded. 64 tokens of 14 + 2 heads take 3.3 us: a launch and that chain.
+// is bounded. 64 tokens of 14 + 2 heads take 3.2 us in replays, 4.6 as calls: a
+// launch and that chain.
 #include <cerrno>
 #include <initializer_list>
 

@@ -15,9 +15,10 @@
 // waiting for one CTA to publish them. No CTA reads what another writes: a
 // slot of a new page takes its page from the free list, by the formula above,
 // not from the table entry that another CTA stores, and arrays that overlap one
-// that is written are refused. Measured: 3.5 us for 64
-// decoding sequences and 16 layers, 4.2 us for 256 sequences (12 of them
-// prompts), 24 layers and 12000 tokens.
+// that is written are refused. Measured in graph
+// replays (and as calls one after the other, which the host's 3 us a call and
+// the launch set): 3.3 us (5.1) for 64 decoding sequences and 16 layers, 4.0 us
+// (6.1) for 256 sequences (12 of them prompts), 24 layers and 12000 tokens.
 #include <cerrno>
 #include <climits>
 
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kTablesThreads) step_tables_kernel(const Table
 
   // Positions and slots: one token a thread, its layers in a loop, the pages of
   // kAtOnce of them asked for together (one after the other they took 5.5 us
-  // instead of 4.2 for 256 sequences, 24 layers and 12000 tokens).
+  // instead of 4.2, in replays, for 256 sequences, 24 layers and 12000 tokens).
   const int t = blockIdx.x * kTablesThreads + tid;
   if (t < p.capacity) {
     const int l0 = blockIdx.y * p.layers_per_cta, l1 = min(l0 + p.layers_per_cta, p.num_layers);
