@@ -487,10 +487,12 @@ size_t paged_pages_workspace_bytes(const pkv_pool_t *pool);
  *   block_tables_out int32 [num_layers][children][max_blocks] out, -1 past a
  *                child's pages;  seq_lens_out int32 [children] out;  shares_out,
  *                free_pages_out, free_head_out out, shaped as their inputs
- *   workspace    device memory of at least paged_pages_workspace_bytes(),
- *                256-byte aligned, ZERO-FILLED before its first use; every call
- *                leaves it ready for the next one of either operation. Calls that
- *                share a workspace must not overlap on the GPU.
+ *   workspace    device memory of workspace_bytes, at least
+ *                paged_pages_workspace_bytes(), 256-byte aligned, ZERO-FILLED
+ *                before its first use and before one with another
+ *                workspace_bytes; every call leaves it ready for the next one of
+ *                either operation, on any pool that it is large enough for. Calls
+ *                that share a workspace must not overlap on the GPU.
  * No array that is written, the workspace and the pool's storage among them, may
  * overlap another one of the call (-EINVAL): pass one call's outputs as the
  * next one's inputs.

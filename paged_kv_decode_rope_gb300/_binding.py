@@ -527,7 +527,8 @@ def paged_pages_workspace_bytes(pool: KVPool) -> int:
 
 def alloc_pages_workspace(pool: KVPool) -> torch.Tensor:
     """A zero-filled workspace for paged_tables_fork and paged_pages_compact on
-    this pool (each call leaves it ready for the next one of either)."""
+    this pool and on any of fewer pages (each call leaves it ready for the next one of
+    either, as long as the whole of it is given)."""
     return torch.zeros(paged_pages_workspace_bytes(pool), dtype=torch.uint8, device=pool.storage.device)
 
 

@@ -66,20 +66,24 @@ struct Chunks {
 };
 
 // The workspace: a word, a word's chunk counts and what each operation keeps a
-// page. `change`, and the marks, are zero between calls.
+// page. `change`, and the marks, are zero between calls; nothing else is, and they are
+// counted from the front, the rest from the back. So calls for pools of any sizes (of n
+// and N pages, n < N) leave what the others need at zero alone: zero up to a place that
+// grows with the pages, anything from one that falls with them, and those of N do not meet.
 struct PagesWorkspace {
   size_t head, counts, change, marks, ranks, movers, places, bytes;
-  explicit PagesWorkspace(long long pages) {
+  // `given`: the bytes that the caller has, the least where it is 0.
+  explicit PagesWorkspace(long long pages, size_t given = 0) {
     auto align256 = [](size_t n) { return (n + 255) / 256 * 256; };
-    const size_t n = static_cast<size_t>(pages);
+    const size_t n = static_cast<size_t>(pages), words = align256(sizeof(int) * n);
     head = 0;
     counts = 256;
     change = counts + sizeof(int2) * kMaxChunks;
-    marks = change + align256(sizeof(int) * n);
-    ranks = marks + align256(2 * n);
-    movers = ranks + align256(sizeof(int) * n);
-    places = movers + align256(sizeof(int) * n);
-    bytes = places + align256(sizeof(int) * n);
+    marks = change + words;
+    bytes = marks + align256(2 * n) + 3 * words;
+    places = (given > bytes ? given / 256 * 256 : bytes) - words;
+    movers = places - words;
+    ranks = movers - words;
   }
 };
 
@@ -893,7 +897,7 @@ int paged_tables_fork(pkv_pool_t* pool, const int32_t* parents, int children, co
     return -EINVAL;
   // (rows and copies are counted in 32 bits)
   if (static_cast<long long>(children) * num_layers * pool->num_kv_heads >= (1ll << 30)) return -EINVAL;
-  const PagesWorkspace at(pool->num_pages);
+  const PagesWorkspace at(pool->num_pages, workspace_bytes);
   if (workspace_bytes < at.bytes) return -EINVAL;
   const long long rows = static_cast<long long>(num_layers) * max_blocks;
   const ByteRange ranges[] = {{block_tables_out, 4 * rows * children},
@@ -901,7 +905,7 @@ int paged_tables_fork(pkv_pool_t* pool, const int32_t* parents, int children, co
                               {shares_out, 4 * pool->num_pages},
                               {free_pages_out, 4ll * num_free},
                               {free_head_out, 4},
-                              {workspace, static_cast<long long>(at.bytes)},
+                              {workspace, static_cast<long long>(workspace_bytes)},
                               {pool->storage, static_cast<long long>(pool->storage_bytes)},
                               {parents, 4ll * children},  // the rest is only read
                               {seq_lens, 4ll * batch},
@@ -973,14 +977,14 @@ int paged_pages_compact(pkv_pool_t* pool, const int32_t* seq_lens, int batch, in
       (num_free > 0 && (!free_pages || !free_pages_out)) || !shares_out || !used || !workspace ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return -EINVAL;
-  const PagesWorkspace at(pool->num_pages);
+  const PagesWorkspace at(pool->num_pages, workspace_bytes);
   if (workspace_bytes < at.bytes) return -EINVAL;
   const long long rows = static_cast<long long>(num_layers) * max_blocks;
   const ByteRange ranges[] = {{block_tables_out, 4 * rows * batch},
                               {shares_out, 4 * pool->num_pages},
                               {free_pages_out, 4ll * num_free},
                               {used, 4},
-                              {workspace, static_cast<long long>(at.bytes)},
+                              {workspace, static_cast<long long>(workspace_bytes)},
                               {pool->storage, static_cast<long long>(pool->storage_bytes)},
                               {seq_lens, 4ll * batch},  // the rest is only read
                               {block_tables, 4 * rows * batch},
