@@ -654,8 +654,9 @@ size_t paged_gqa_decode_shared_workspace_bytes(int batch, int num_q_heads, int n
  * the long way, as it is for little work, where the groups are not looked at.
  * Keys of a bad page are skipped (PKV_ERR_PAGE_ID). Pages before the first key
  * that a tile of rows sees (128 / group members) are neither read nor looked up.
- * A value that is not finite can reach the rows of other members of its
- * group that do not see it. At most two launches. (Not on the pages.)
+ * A value that is not finite reaches the rows that see its key and no others (with
+ * a window, rows that it may have reached are worked out again from their own keys,
+ * which takes long). At most two launches. (Not on the pages.)
  */
 int paged_gqa_decode_shared(const pkv_pool_t *pool, const float *q_rot, void *out, int out_type,
                             const int32_t *block_tables, int max_blocks, const int32_t *seq_lens,

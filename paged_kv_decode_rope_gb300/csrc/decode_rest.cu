@@ -51,6 +51,7 @@ constexpr uint32_t kRing = kWarps * kStages * kHeadPageBytes;
 static_assert(kMaxGroup * kHeadDim * sizeof(float) <= kStages * kHeadPageBytes, "a warp's sums go into its ring");
 
 struct RestParams {
+  const uint8_t* pool;
   long long num_pages;
   int hkv, group;
   const float* q_rot;  // [batch][hq][64]
@@ -71,6 +72,52 @@ struct RestParams {
   int* err;
 };
 
+// Elements e0 .. e1 - 1 of a segment's rows from the sequence's own keys alone, key by
+// key in plain arithmetic, a row a warp. Under a window a tile's rows see different keys,
+// and a value that is not finite makes NaN of the rows whose weight for it is 0, so this
+// is for rows that are not finite. Small and inlined: as a function that is called, or as
+// the loop over the ring a second time, it made every call with a window 3% slower.
+__device__ __forceinline__ void finish_alone(const RestParams& p, int b, int h, int e0, int e1) {
+  const int lane = threadIdx.x & 31, n = p.seq_lens[b], lo = max(n - p.window, 0);
+  const int32_t* bt = p.block_tables + static_cast<size_t>(b) * p.max_blocks;
+  for (int g = e0 / kHeadDim + (threadIdx.x >> 5); g * kHeadDim < e1; g += kWarps) {
+    const size_t row = (static_cast<size_t>(b) * p.hkv + h) * p.group + g;
+    const float2 q = *reinterpret_cast<const float2*>(p.q_rot + row * kHeadDim + 2 * lane);
+    const float slope = p.slopes ? p.slopes[h * p.group + g] * kLog2e : 0.f;
+    float m = -INFINITY, l = 0.f, o[2] = {0.f, 0.f};  // dims 2 lane and 2 lane + 1
+    for (int key = lo; key < n; ++key) {
+      const int page = bt[key / kPage];
+      if (page < 0 || page >= p.num_pages) continue;  // (reported where it was met first)
+      const uint8_t* at = p.pool + (static_cast<size_t>(page) * p.hkv + h) * kHeadPageBytes + key % kPage * kRowBytes + 4 * lane;
+      const float2 k = bf16x2_to_float2(*reinterpret_cast<const uint32_t*>(at));
+      const float2 v = bf16x2_to_float2(*reinterpret_cast<const uint32_t*>(at + kHalfBytes));
+      float s = q.x * p.qscale * k.x + q.y * p.qscale * k.y;
+#pragma unroll
+      for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(kFull, s, i);
+      if (p.cap.cap > 0.f) s = capped_score(p.cap, s);
+      s -= slope * static_cast<float>(n - 1 - key);
+      const float up = fmaxf(m, s), ref = up == -INFINITY ? 0.f : up;
+      const float keep = fast_exp2(m - ref), w = fast_exp2(s - ref);
+      m = up;
+      l = l * keep + w;
+      o[0] = o[0] * keep + w * v.x;
+      o[1] = o[1] * keep + w * v.y;
+    }
+    for (int i = 0; i < 2; ++i) {
+      const int d = 2 * lane + i, e = g * kHeadDim + d;
+      if (e < e0 || e >= e1) continue;
+      const float y = l == 0.f ? 0.f : o[i] / l;
+      if (p.out_bf16) {
+        static_cast<uint16_t*>(p.out)[row * kHeadDim + d] = static_cast<uint16_t>(pack_bf16x2(y, 0.f));
+      } else {
+        static_cast<float*>(p.out)[row * kHeadDim + d] = y;
+      }
+    }
+  }
+}
+
+// kWindow: whether there is one (p.window > 0).
+template <bool kWindow>
 __global__ void __launch_bounds__(kThreads, kCtas)
     decode_rest_kernel(const __grid_constant__ CUtensorMap kv_map, const RestParams p) {
   extern __shared__ __align__(1024) uint8_t dsmem[];
@@ -125,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       if (s_least != INT_MAX) first = max(min(s_group.z, s_least), 0) / kPage;
     }
   }
-  const bool shares = first > 0;
+  const bool bad = n < 1 || n > p.max_blocks * kPage, shares = first > 0 && !bad;
   // Q as the A operand of the four steps: head g8's dims 16 t4 + 4 s .. + 3
   uint32_t aq[4][4];
 #pragma unroll
@@ -143,9 +190,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     aq[s][3] = pack_bf16x2(x.z - r1.x, x.w - r1.y);
   }
   const float slope = p.slopes && g8 < G ? p.slopes[h * G + g8] * kLog2e : 0.f;
-  const bool bad = n < 1 || n > p.max_blocks * kPage;
   if (bad && rank == 0 && tid == 0) atomicOr(p.err, PKV_ERR_SEQ_LEN);
-  const int lo = p.window > 0 ? max(n - p.window, 0) : 0;
+  const int lo = kWindow ? max(n - p.window, 0) : 0;
   // pages first .. last - 1; none for a bad length
   first = max(first, lo / kPage);
   const int last = bad ? first : max((n + kPage - 1) / kPage, first);
@@ -341,8 +387,10 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   }
   __syncthreads();
   // element i of the segment's G rows: head g = i / 64, dim i % 64
+  [[maybe_unused]] bool lost = false;
   auto finish = [&](int i, float sum, float total) {
     const float y = total == 0.f ? 0.f : sum / total;  // (a NaN score makes the row NaN)
+    if constexpr (kWindow) lost |= !isfinite(y);
     if (p.out_bf16) {
       static_cast<uint16_t*>(p.out)[row0 * kHeadDim + i] = static_cast<uint16_t>(pack_bf16x2(y, 0.f));
     } else {
@@ -371,7 +419,15 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       }
     }
   }
-  if (alone) return;
+  // whether elements e0 .. e1 - 1, this CTA's, need finish_alone, and that
+  auto finish_lost = [&](int e0, int e1) {
+    if constexpr (kWindow)
+      if (__syncthreads_or(lost && shares)) finish_alone(p, b, h, e0, e1);
+  };
+  if (alone) {
+    finish_lost(0, G * kHeadDim);
+    return;
+  }
   cluster.sync();
   // each CTA finishes its share of the rows
   const int share = (G * kHeadDim + ctas - 1) / ctas;
@@ -400,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     }
     finish(i, sum, total);
   }
+  finish_lost(rank * share, min((rank + 1) * share, G * kHeadDim));
   cluster.sync();  // no CTA leaves while another reads its sums
 }
 
@@ -421,6 +478,7 @@ cudaLaunchConfig_t config(cudaLaunchAttribute (&attr)[2], int segments, int ctas
 
 // Clusters of `ctas` CTAs that run at once (fewer than the CTAs that fit over
 // `ctas`: see decode_small.cu); -1: a CUDA call failed.
+template <bool kWindow>
 int clusters_at_once(int device, int ctas) {
   static std::atomic<int> cache[64][kMaxCluster + 1];  // found + 1
   std::atomic<int>& known = cache[device & 63][ctas];
@@ -429,26 +487,45 @@ int clusters_at_once(int device, int ctas) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = config(attr, 1, ctas, nullptr);
   cfg.numAttrs = 1;  // the cluster's
-  if (cudaOccupancyMaxActiveClusters(&n, decode_rest_kernel, &cfg) != cudaSuccess) return -1;
+  if (cudaOccupancyMaxActiveClusters(&n, decode_rest_kernel<kWindow>, &cfg) != cudaSuccess) return -1;
   known.store(n + 1, std::memory_order_relaxed);
   return n;
+}
+
+template <bool kWindow>
+cudaError_t launch(const CUtensorMap& kv_map, const RestParams& p, cudaStream_t stream) {
+  static DeviceSetup setup;
+  cudaError_t e = setup([] {
+    cudaError_t e = cudaFuncSetAttribute(decode_rest_kernel<kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024);
+    if (e != cudaSuccess) return e;
+    // more CTAs a cluster than every GPU has to grant
+    return cudaFuncSetAttribute(decode_rest_kernel<kWindow>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
+  int device = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const int segments = p.batch * p.hkv;
+  // the most CTAs a segment with which all segments run at once, a power of two: 24
+  // sequences of 2240 tokens in 2 CTAs a segment 19.0 us, in 3 23.0; 5 of 16040 in 8 20.7, in
+  // 15 26.5; 20 of 2300 in 2 19.2, in 3 18.1 (32 + 8 heads, one prompt, both kernels)
+  int ctas = p.max_blocks > kShortPages ? kMaxCluster : 8;
+  for (; ctas > 1; ctas /= 2) {
+    const int most = clusters_at_once<kWindow>(device, ctas);
+    if (most < 0) return cudaGetLastError();
+    if (segments <= most) break;
+  }
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = config(attr, segments, ctas, stream);
+  return cudaLaunchKernelEx(&cfg, decode_rest_kernel<kWindow>, kv_map, p);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_rest(const SharedLaunch& a, const SharedPieces& pieces, cudaStream_t stream) {
-  static DeviceSetup setup;
-  cudaError_t e = setup([] {
-    cudaError_t e = cudaFuncSetAttribute(decode_rest_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024);
-    if (e != cudaSuccess) return e;
-    // more CTAs a cluster than every GPU has to grant
-    return cudaFuncSetAttribute(decode_rest_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  });
-  int device = 0;
-  if (e == cudaSuccess) e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return e;
   constexpr double log2e = 1.4426950408889634;
   RestParams p = {};
+  p.pool = a.pool;
+  p.pool = a.pool;
   p.num_pages = a.num_pages;
   p.hkv = a.num_kv_heads;
   p.group = a.num_q_heads / a.num_kv_heads;
@@ -468,19 +545,7 @@ cudaError_t launch_decode_rest(const SharedLaunch& a, const SharedPieces& pieces
   p.shared_lens = a.shared_lens;
   p.groups = a.groups;
   p.err = a.err;
-  const int segments = a.batch * a.num_kv_heads;
-  // the most CTAs a segment with which all segments run at once, a power of two: 24
-  // sequences of 2240 tokens in 2 CTAs a segment 19.0 us, in 3 23.0; 5 of 16040 in 8 20.7, in
-  // 15 26.5; 20 of 2300 in 2 19.2, in 3 18.1 (32 + 8 heads, one prompt, both kernels)
-  int ctas = a.max_blocks > kShortPages ? kMaxCluster : 8;
-  for (; ctas > 1; ctas /= 2) {
-    const int most = clusters_at_once(device, ctas);
-    if (most < 0) return cudaGetLastError();
-    if (segments <= most) break;
-  }
-  cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = config(attr, segments, ctas, stream);
-  return cudaLaunchKernelEx(&cfg, decode_rest_kernel, *a.kv_map, p);
+  return a.window > 0 ? launch<true>(*a.kv_map, p, stream) : launch<false>(*a.kv_map, p, stream);
 }
 
 }  // namespace pkv

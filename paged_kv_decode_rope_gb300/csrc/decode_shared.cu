@@ -26,7 +26,9 @@
 // every piece puts its rows' m, l and O into the workspace. A piece's place needs no
 // counting: tile and CTA only ever go up along the line, so (first row of the tile)
 // + 128 * CTA is free. The sequences' own pages are the second kernel's, which joins
-// the pieces too (decode_rest.cu).
+// the pieces too (decode_rest.cu). Under a window a tile's rows see different keys, and a
+// value that is not finite makes NaN of the rows whose weight for it is 0: the second
+// kernel works rows that are not finite out from their own keys alone.
 //
 // Warps 0-7 run the softmax and the epilogue; of 8-11, which hand registers to
 // them, 8 copies keys (and finds the tiles), 11 values, 9 issues the score
