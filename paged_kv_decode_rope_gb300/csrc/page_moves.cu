@@ -30,6 +30,7 @@
 // us). Compaction of half a pool (18144 pages held, 11400 of 32 KB moved) 129 us, of
 // which the contents are 113 (5.9 TB/s read and written, 88% of a copy's rate); of 8
 // sequences 16.
+#include <atomic>
 #include <cerrno>
 #include <climits>
 
@@ -827,9 +828,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) compact_move_kernel(c
 // ---------------------------------------------------------------------------
 
 // Launch with programmatic stream serialization, as one cluster or without clusters.
-template <typename P>
-cudaError_t launch_after(void (*kernel)(P), int grid, size_t smem, cudaStream_t stream, const P& p, bool one_cluster = false) {
-  cudaLaunchAttribute attr[2];
+cudaLaunchConfig_t config(cudaLaunchAttribute (&attr)[2], int grid, size_t smem, cudaStream_t stream, bool one_cluster) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -842,7 +841,33 @@ cudaError_t launch_after(void (*kernel)(P), int grid, size_t smem, cudaStream_t 
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = one_cluster ? 2 : 1;
+  return cfg;
+}
+template <typename P>
+cudaError_t launch_after(void (*kernel)(P), int grid, size_t smem, cudaStream_t stream, const P& p, bool one_cluster = false) {
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = config(attr, grid, smem, stream, one_cluster);
   return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// Whether `device`, the current one, runs a cluster of kCluster CTAs of `kernel`, the
+// only one asked for of its type P. (Eight are what every GPU grants; a part of a GPU may
+// have no 16 SMs that a cluster can take.)
+template <typename P>
+bool cluster_runs(void (*kernel)(P), size_t smem, int device) {
+  static std::atomic<int> known[64];  // by device: 1 yes, -1 no; any further device is asked in every call
+  if (device < 64)
+    if (const int k = known[device].load(std::memory_order_relaxed)) return k > 0;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = config(attr, kCluster, smem, nullptr, true);
+  cfg.attrs = attr + 1;  // the cluster's
+  cfg.numAttrs = 1;
+  int n = 0;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+  if (e != cudaSuccess) return cudaGetLastError(), false;  // the launches by grids say what there is to say
+  if (device < 64) known[device].store(n > 0 ? 1 : -1, std::memory_order_relaxed);
+  return n > 0;
 }
 
 int failed(cudaError_t e) {
@@ -948,14 +973,13 @@ int paged_tables_fork(pkv_pool_t* pool, const int32_t* parents, int children, co
   const cudaStream_t on = static_cast<cudaStream_t>(stream);
   static DeviceSetup setup;
   cudaError_t e = setup([&] {
-    cudaError_t e = cudaFuncSetAttribute(fork_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(fork_smem(PKV_TABLES_MAX_BATCH, PKV_TABLES_MAX_BATCH)));
-    return e == cudaSuccess ? cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : e;
+    return cudaFuncSetAttribute(fork_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(fork_smem(PKV_TABLES_MAX_BATCH, PKV_TABLES_MAX_BATCH)));
   });
   if (e != cudaSuccess) return failed(e);
   const long long copies = static_cast<long long>(children) * num_layers * pool->num_kv_heads;  // at most
   const long long units = copies + (static_cast<long long>(batch) + children) * num_layers * parts_of(max_blocks);
-  if (one_cluster(cut, units, kForkUnits)) {
+  if (one_cluster(cut, units, kForkUnits) && cluster_runs(fork_kernel, fork_smem(kForkUnits, 0), pool->device)) {
     e = launch_after(fork_kernel, kCluster, fork_smem(batch, children), on, p, true);
     return e == cudaSuccess ? 0 : failed(e);
   }
@@ -1026,10 +1050,8 @@ int paged_pages_compact(pkv_pool_t* pool, const int32_t* seq_lens, int batch, in
   p.err = pool->d_err;
   const cudaStream_t on = static_cast<cudaStream_t>(stream);
   const long long units = static_cast<long long>(num_layers) * batch * parts_of(max_blocks), list_units = parts_of(num_free);
-  static DeviceSetup setup;
-  cudaError_t e = setup([&] { return cudaFuncSetAttribute(compact_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
-  if (e != cudaSuccess) return failed(e);
-  if (one_cluster(cut, units + list_units, kPlanUnits)) {
+  cudaError_t e = cudaSuccess;
+  if (one_cluster(cut, units + list_units, kPlanUnits) && cluster_runs(compact_plan_kernel, 0, pool->device)) {
     e = launch_after(compact_plan_kernel, kCluster, 0, on, p, true);
   } else {
     e = launch_after(compact_mark_kernel, grid_for(units > list_units ? units : list_units, 4, sms), 0, on, p);
