@@ -51,7 +51,7 @@ constexpr int kWarpPages = 256;  // consecutive pages that a warp looks at: a ba
 constexpr int kBallots = kWarpPages / 32;
 constexpr int kRoundPages = kMoveWarps * kWarpPages;  // 2048
 constexpr int kMaxChunks = 1024;
-constexpr int kCluster = 16;  // CTAs, of a chunk each at most, of the launches that are one cluster
+constexpr int kCluster = 16;  // CTAs of the launches that are one cluster
 constexpr int kMaxLayers = 4096;  // (rows of the tables are counted in 32 bits)
 
 // The pages cut into at most kMaxChunks chunks of whole rounds.
@@ -881,19 +881,26 @@ int grid_for(long long warps, int most, int sms) {
   return static_cast<int>(n < 1 ? 1 : n < static_cast<long long>(most) * sms ? n : static_cast<long long>(most) * sms);
 }
 
-// A warp's pieces of work (copies and parts of rows) up to which a pool of 16 chunks or
-// fewer is taken in one cluster. Measured, one cluster against a grid a kernel, graph
-// replays / calls in a row:
-//   fork of 640 pieces (4 beams of 1100 tokens, 16 layers, 8 kv heads) 7.3 / 8.2 us
-//   against 7.4 / 12.9, of 4 pieces 6.1 / 8.3 against 6.4 / 12.9; of 1024 9.1 / 9.2
-//   against 7.4 / 12.0, of 1280 8.8 / 9.0 against 7.4 / 12.3, of 2560 11.2 / 11.4 against
-//   7.4 / 12.3
-//   compaction of 180 pieces (8 sequences of 700 tokens, 16 layers, 12000 pages) 15.1 /
-//   15.3 against 15.5 / 16.4; of 320 (30000 pages) 18.4 / 18.9 against 17.7 / 19.0, of 560
-//   15.4 / 15.8 against 13.9 / 14.7
-constexpr long long kForkUnits = 768, kPlanUnits = 256;
+// When a call is one cluster: by the pool's chunks and a warp's pieces of work (a fork's
+// copies and parts of rows, five a warp; a compaction's parts of rows and of the list).
+// Measured, one cluster against a grid a kernel, graph replays / calls in a row, us, all
+// of the pool listed:
+//   fork, 2048 pages       16 pieces  6.3 /  6.3 against  7.0 /  8.0; 640  6.9 /  6.9 against  7.5 /  8.4
+//        12000             16         7.3 /  7.3          7.0 /  7.8  640  7.7 /  7.7          7.5 /  8.3
+//                                                                     800  8.7 /  8.7          7.6 /  8.3
+//        25000             16         8.0 /  8.0          7.0 /  7.9  640  8.3 /  8.5          7.6 /  8.4
+//        30000             16         8.7 /  8.7          7.0 /  7.9  640  9.2 /  9.2          7.6 /  8.5
+//   compaction, 2048       17        10.3 / 10.7         11.9 / 13.2  112 10.6 / 10.9         11.3 / 12.2
+//        12000             95        11.2 / 11.6         11.9 / 12.7  214 14.0 / 14.3         13.8 / 15.0
+//                         286        15.2 / 15.4         14.9 / 15.6  350 15.4 / 15.7         14.9 / 15.9
+//        25000            197        12.7 / 13.1         12.2 / 13.3  292 15.1 / 15.5         14.7 / 15.6
+//        30000            236        13.4 / 13.7         12.3 / 13.2  331 15.5 / 15.8         14.7 / 15.8
+// so that calls gain up to some 25000 pages, replays up to some 8000.
+constexpr int kClusterChunks = 12;
+constexpr long long kForkUnits = 5 * kCluster * kMoveWarps, kPlanUnits = 256;
+static_assert(kClusterChunks <= kCluster, "a chunk a CTA at most");
 bool one_cluster(const Chunks& cut, long long units, long long most) {
-  return cut.n <= kCluster && units <= most;
+  return cut.n <= kClusterChunks && units <= most;
 }
 
 size_t fork_smem(int batch, int children) { return sizeof(int) * (3 * static_cast<size_t>(batch) + 3 * static_cast<size_t>(children)); }

@@ -43,9 +43,9 @@ int main(int, char** argv) {
   auto run = [&](const char* what, int device, long long pages, int batch, int listed) {
     static pkv_pool pool;
     pool.storage = at(1);
-    pool.storage_bytes = 4096 * pages;
+    pool.storage_bytes = 3 * 4096 * pages;
     pool.num_pages = pages;
-    pool.num_kv_heads = 1;
+    pool.num_kv_heads = 3;
     pool.device = g_device = device;
     g_launches.clear();
     const int rc = *what == 'f' ? fork(&pool, at(2), batch, at(3), batch, 1, at(4), 100, at(5), at(6), listed, at(7), at(8), at(9), at(10),
@@ -57,16 +57,16 @@ int main(int, char** argv) {
   };
   for (const char* what : {"fork", "compaction"}) {
     g_asked = 0;
-    const int most = *what == 'f' ? 256 : 250, list = 6 * 128;  // 768 pieces of work; 256
+    const int most = *what == 'f' ? 128 : 250, list = 6 * 128;  // 640 pieces of work; 256
     g_clusters = 5;
-    run(what, 0, 32768, most, list);
-    run(what, 0, 32768, most + 1, list);  // too much work
-    run(what, 0, 32769, most, list);      // too many chunks
+    run(what, 0, 24576, most, list);
+    run(what, 0, 24576, most + 1, list);  // too much work
+    run(what, 0, 24577, most, list);      // too many chunks
     run(what, 0, 2048, most, list);
     g_clusters = 0;  // a device that runs none
-    run(what, 1, 32768, most, list);
+    run(what, 1, 24576, most, list);
     run(what, 1, 2048, 1, list);
-    run(what, 0, 32768, most, list);  // the other one still does
+    run(what, 0, 24576, most, list);  // the other one still does
     g_answer = cudaErrorInvalidValue;  // no answer
     run(what, 2, 2048, 1, list);
     g_answer = cudaSuccess;

@@ -1,5 +1,5 @@
-"""Forks and compactions that are one cluster, in pools of up to as many chunks (of 2048
-pages) as it has CTAs, and by grids on the other side of that border. Which call is which
+"""Forks and compactions that are one cluster, in pools of up to 12 chunks (of 2048
+pages), and by grids on the other side of that border. Which call is which
 is test_page_launches.py's."""
 import numpy as np
 import pytest
@@ -7,8 +7,8 @@ import pytest
 from tests.test_gpu_page_moves import Cache, check_compact, check_fork
 from tests.test_gpu_pages_workspace import marks_are_zero
 
-CHUNK, MOST = 2048, 16
-POOLS = [CHUNK + 1, 3 * CHUNK, 6 * CHUNK + 5, 11 * CHUNK - 1, 15 * CHUNK, MOST * CHUNK - 1, MOST * CHUNK, MOST * CHUNK + 1]
+CHUNK, MOST = 2048, 12
+POOLS = [CHUNK + 1, 3 * CHUNK, 6 * CHUNK + 5, 9 * CHUNK - 1, 11 * CHUNK, MOST * CHUNK - 1, MOST * CHUNK, MOST * CHUNK + 1]
 
 
 @pytest.mark.gpu
@@ -19,7 +19,7 @@ POOLS = [CHUNK + 1, 3 * CHUNK, 6 * CHUNK + 5, 11 * CHUNK - 1, 15 * CHUNK, MOST *
     ([16 * 300, 33, 16 * 40 + 1], [2, 0, 2, 2])])
 def test_forks(pages, lens, parents):
     c = Cache(lens, layers=1, hkv=1, pages=pages, seed=pages)
-    assert len(parents) + (len(lens) + len(parents)) * -(-c.tables.shape[2] // 128) <= 768
+    assert len(parents) + (len(lens) + len(parents)) * -(-c.tables.shape[2] // 128) <= 640
     for _ in range(2):
         check_fork(c, parents)
         check_fork(c, [])  # everything is given back
