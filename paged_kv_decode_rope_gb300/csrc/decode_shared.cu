@@ -1010,10 +1010,16 @@ size_t shared_workspace_bytes(int batch, int num_q_heads, int sm_count) {
 
 cudaError_t launch_decode_shared(const SharedLaunch& a, cudaStream_t stream) {
   // Little work is done without sharing, by the scored decode's kernel for it: reading
-  // it all takes no longer than the two kernels' latencies. Measured there and with
-  // the shared kernels, 32 + 8 heads: 8 sequences of 940 tokens 6.5 against 14.3 us, 4
-  // of 8040 12.0 / 21.2, 16 of 2040 12.0 / 16.0, 32 of 1240 (8 prompts) 15.8 / 16.0;
-  // 14 + 2 heads, 64 of 4040 tokens, past the rule: 19.4 (the general kernel) / 19.3.
+  // it all takes no longer than the two kernels' latencies. Calls measured there and with
+  // the shared kernels, us, tables filled, half of the tokens shared by all of 4, 16 and 64
+  // sequences:
+  //   32 + 8 heads, 20000 pages in all  14.2 / 25.2  13.9 / 20.0  16.9 / 18.0
+  //                 25000               16.8 / 29.9  16.4 / 21.6  18.3 / 18.9
+  // and over 60 batches of 4 to 256, 32 + 8, 14 + 2 and 8 + 8 heads, half to nine tenths
+  // shared, by one group or many, the shared kernels' time in the other's (the mean, least
+  // and most): 32000 pages 1.12 (0.70 to 1.62), 40000 1.02 (0.60 to 1.49), 50000 0.92 (0.54
+  // to 1.38); with tables half filled 40000 1.37 (0.87 to 1.84), 65000 1.12 (0.69 to 1.62).
+  constexpr long long kMostPages = 32768;
   DecodeLaunch all = {};
   all.pool = a.pool;
   all.num_pages = a.num_pages;
@@ -1031,7 +1037,7 @@ cudaError_t launch_decode_shared(const SharedLaunch& a, cudaStream_t stream) {
   all.window = a.window;
   all.out_bf16 = a.out_bf16;
   all.err = a.err;
-  if (decode_small_fits(all)) return launch_decode_small(all, stream);
+  if (decode_small_fits(all, kMostPages)) return launch_decode_small(all, stream);
   SharedPieces to = pieces_in(a.workspace, a.batch, a.num_q_heads, kCtas * a.sm_count);
   if (a.groups == 0) {
     to.ctas = 0;  // no pieces

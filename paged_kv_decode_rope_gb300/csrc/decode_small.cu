@@ -360,9 +360,10 @@ constexpr long long kMostPages = 20480, kMostSegmentPages = 2048;
 static int segment_pages(const DecodeLaunch& a) {
   return a.window > 0 && a.window / kPage + 2 < a.max_blocks ? a.window / kPage + 2 : a.max_blocks;
 }
-bool decode_small_fits(const DecodeLaunch& a) {
+bool decode_small_fits(const DecodeLaunch& a) { return decode_small_fits(a, kMostPages); }
+bool decode_small_fits(const DecodeLaunch& a, long long most_pages) {
   const long long pages = segment_pages(a);
-  return pages <= kMostSegmentPages && pages * a.batch * a.num_kv_heads <= kMostPages;
+  return pages <= kMostSegmentPages && pages * a.batch * a.num_kv_heads <= most_pages;
 }
 
 cudaError_t launch_decode_small(const DecodeLaunch& a, cudaStream_t stream) {

@@ -144,8 +144,10 @@ constexpr int kDecodeBatchChunk = 2048;
 size_t decode_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int max_blocks,
                               int pages_per_split, int sm_count);
 cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t stream);
-// The scored decode for little work (decode_small.cu), and whether this is little.
+// The scored decode for little work (decode_small.cu), and whether this is little
+// (`most_pages`: beside a kernel other than the scored decode's general one).
 bool decode_small_fits(const DecodeLaunch& a);
+bool decode_small_fits(const DecodeLaunch& a, long long most_pages);
 cudaError_t launch_decode_small(const DecodeLaunch& a, cudaStream_t stream);
 // Decode of groups of sequences that share their first pages (decode_shared.cu).
 struct SharedLaunch {

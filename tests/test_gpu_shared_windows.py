@@ -76,9 +76,8 @@ def test_few_members_of_long_windows(hq, hkv, past, softcap, alibi, dtype):
 @pytest.mark.parametrize("window,least,most", [(300, 600, 640), (300, 601, 900), (257, 640, 2000), (320, 100, 700)])
 def test_many_members_of_short_windows(window, least, most, softcap, alibi, dtype):
     g = torch.Generator().manual_seed(window + least)
-    lens = torch.randint(least, most + 1, (200,), generator=g).tolist()
+    lens = torch.randint(least, most + 1, (260,), generator=g).tolist()
     b = Batch(16, 8, [(600, lens), (None, [window + 40])], 3, window)
-    assert (window // PAGE + 2) * 201 * 8 > 20480
     assert bool(check(b, dtype, softcap, alibi).all())
     b.pool.close()
 
