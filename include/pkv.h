@@ -638,8 +638,9 @@ size_t paged_gqa_decode_shared_workspace_bytes(int batch, int num_q_heads, int n
  *                [groups], in tokens;  0 <= groups <= batch
  *   q_rot        fp32 [batch][num_q_heads][64], 16-byte aligned
  *   out          [batch][num_q_heads][64] of out_type, 16-byte aligned. With
- *                PKV_BF16 the softmax weights are rounded to bf16 as well (and
- *                summed as rounded); with PKV_F32 they keep 16 bits.
+ *                PKV_BF16 the softmax weights of pages that are read once for a
+ *                group are rounded to bf16 (and summed as rounded); all others,
+ *                and with PKV_F32 these too, keep 16 bits.
  *   block_tables int32 [batch][max_blocks];  seq_lens int32 [batch] (>= 1).
  *                batch <= PKV_SHARED_MAX_BATCH, max_blocks <= PKV_SHARED_MAX_BLOCKS
  *   workspace    device memory of at least

@@ -18,7 +18,9 @@
 //   O += P V (+ P_lo V),  l += P 1
 // Q enters as bf16 with its bf16 remainder, as everywhere in this library, P too
 // where the output is fp32 (kPair); with a bf16 output P is rounded once and its
-// row sums come from a product with ones, of the rounded P.
+// row sums come from a product with ones, of the rounded P. That makes an error of 1.2e-3
+// to 1.5e-3 of the output's norm beside the 1.66e-3 of rounding the output, and saves 13%
+// (256 sequences behind three documents 144 us against 166).
 //
 // All steps of all tiles form one line (kv head by kv head, tile by tile), which is
 // cut evenly over the CTAs, two an SM: every CTA works the line's prefix sums out
@@ -36,7 +38,7 @@
 //
 // Measured in graph replays with the second kernel, bf16 out (fp32): 256 rows behind
 // one prompt of 32768 tokens, 8 kv heads, 123 us (146), 151 (185) with a cap; with every
-// sequence reading all of it, 1630 us for 256 behind three documents that take 145
+// sequence reading all of it, 1630 us for 256 behind three documents that take 144
 // here. A step takes an SM 850 cycles (1000), of 128 rows or 16: what bounds it is
 // neither the tensor core alone (600 cycles of products of N = 64, which take their A
 // operand at half the rate that N = 128 would) nor the issue of the softmax (some 250

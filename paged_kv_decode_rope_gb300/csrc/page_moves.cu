@@ -22,12 +22,12 @@
 // counted by chunks; movers and places ranked; contents, tables, counts and list
 // written. Here too the first three are one cluster for little work.
 //
-// Measured in graph replays: a fork of 4 beams 6.3 us, of 64 x 4 (16 layers, 8 kv heads;
-// 40 MB of tables, counts and copies) 14.8, of 16 prompts into 8 each (24 layers) 11.8:
-// launches and, in each kernel, two or three reads one after the other. What the list
-// kernel reads is asked for together, and the list is copied by CTAs of its own beside
+// Measured in graph replays: a fork of 4 beams in a pool of 2500 pages 6.3 us (in others:
+// see kForkUnits), of 64 x 4 (16 layers, 8 kv heads; 40 MB of tables, counts and copies)
+// 14.9, of 16 prompts into 8 each (24 layers) 11.9: launches and, in each kernel, two or
+// three reads one after the other. What the list kernel reads is asked for together, and the list is copied by CTAs of its own beside
 // those that write the counts (one after the other in the same CTAs: 9.1, 18.8 and 15.1
-// us). Compaction of half a pool (18144 pages held, 11400 of 32 KB moved) 129 us, of
+// us). Compaction of half a pool (18144 pages held, 11400 of 32 KB moved) 128 us, of
 // which the contents are 113 (5.9 TB/s read and written, 88% of a copy's rate); of 8
 // sequences 16.
 #include <atomic>

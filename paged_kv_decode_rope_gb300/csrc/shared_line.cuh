@@ -6,7 +6,11 @@
 
 namespace pkv {
 
-constexpr int kUnitCost = 4;  // what a tile costs besides its steps, in steps
+// What a tile costs besides its steps, in steps. With 1, 2, 4 and 8: 256 sequences behind
+// 2000 tokens 38.3, 37.8, 35.9 and 36.7 us, behind three documents 127.3, 127.0, 125.7 and
+// 125.9, 64 prompts of 4 beams 37.6, 37.4, 36.7 and 37.2, 30 of 8 answers 53.6, 53.4, 53.7
+// and 55.3.
+constexpr int kUnitCost = 4;
 constexpr int kStepKeys = 64, kStepPages = kStepKeys / kPage;
 
 // A sequence's shared blocks and its place in its tile in one word.
